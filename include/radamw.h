@@ -588,6 +588,172 @@ int radamw_lists_fused_step(const radamw_list *lists, int32_t nlists, uint64_t *
 int radamw_host_coefficients(const radamw_options *opts, uint64_t t, double gradient_scale,
                              float *out9);
 
+/*
+ * ---------------------------------------------------- vocabulary operators --
+ *
+ * The two ends of the training step that the optimizer closes: the embedding
+ * lookup with its gradient, and the losses over the vocabulary's logits with
+ * theirs.  Both are indexed by token ids and both move arrays of the
+ * vocabulary's size.  Their gradients go where the update reads them: the
+ * embedding gradient into a dense gradient (of a bucket, too), the logits'
+ * gradient scaled by the loss scale the update divides out again
+ * (radamw_control.gradient_scale).
+ *
+ * Conventions beyond the general ones:
+ *   - Two-dimensional arrays are row-major with unit column stride; `stride`
+ *     counts the elements between row starts (stride >= row width), so a row
+ *     may start at any element.  Spans are checked as (n - 1) * stride +
+ *     width elements, and a written span may overlap no other span.
+ *   - Index arrays hold 32- or 64-bit integers (radamw_index_type).  Their
+ *     VALUES are read on the device only: an id or label outside its range
+ *     is not an error but takes no part, as stated at each call.
+ *   - Sums, softmax statistics and losses are formed in FP32 or FP64;
+ *     outputs of a 16-bit type are rounded once, to nearest even.
+ *   - No atomics on values: every sum has a fixed order, so repeated calls
+ *     on the same inputs give identical bits.
+ *   - Like every entry point they refuse a stream under graph capture.
+ *   - Calls keep nothing: two calls may run at once, on any streams, as long
+ *     as they share no output and no workspace.
+ *   - Limits (RADAMW_ERR_RANGE): dim <= 2^24, vocab <= 2^27, rows and n below
+ *     2^31 and such that a launch needs at most 2^24 - 1 workgroups (n up to
+ *     2^24 - 1 always fits for the losses and the lookup).
+ */
+typedef enum {
+    RADAMW_I32 = 0,
+    RADAMW_I64 = 1
+} radamw_index_type;
+
+/*
+ * Scaled embedding lookup:
+ *   out[t, :] = scale * table[ids[t], :],   t = 0 .. n-1
+ * in FP32, rounded once to out_dtype; a row of zeros where ids[t] is outside
+ * 0 .. rows-1.
+ *   table : [rows, dim] of table_dtype (FP32 masters, or their 16-bit model
+ *           copy), row stride table_stride.
+ *   ids   : n indices.   out : [n, dim] of out_dtype, row stride out_stride.
+ * scale is finite, also as FP32.  n == 0 launches nothing.  rows may be 0
+ * (every output row is zeros).
+ */
+int radamw_embedding_lookup(const void *table, radamw_dtype table_dtype, int64_t rows, int64_t dim,
+                            int64_t table_stride, const void *ids, radamw_index_type ids_type, int64_t n, double scale,
+                            void *out, radamw_dtype out_dtype, int64_t out_stride, radamw_stream_t stream);
+
+/*
+ * Gradient of the lookup with respect to the table:
+ *   table_grad[v, :] = (accumulate ? table_grad[v, :] : 0)
+ *                      + scale * sum of grad_out[t, :] over ids[t] == v
+ * The token positions are sorted by id (stably) and each id's rows are
+ * summed in FP32 in a fixed order; the result is rounded once.  Tokens whose
+ * id is padding_id (-1: none) or outside 0 .. rows-1 add nothing.
+ *   accumulate = 0 : all rows of table_grad are written (zeros where no token
+ *                    adds).  Columns between dim and table_stride are left.
+ *   accumulate = 1 : only rows that some token names are read and written,
+ *                    the form that adds into a gradient bucket.
+ *   workspace      : device, 16-byte aligned, at least
+ *                    radamw_embedding_grad_workspace_bytes(n, rows, dim);
+ *                    its contents need no preparation and mean nothing
+ *                    afterwards.  In use until the stream has passed the call.
+ * The workspace size returns a negative status for arguments out of range.
+ */
+int64_t radamw_embedding_grad_workspace_bytes(int64_t n, int64_t rows, int64_t dim);
+int radamw_embedding_grad(const void *grad_out, radamw_dtype grad_dtype, int64_t grad_stride, const void *ids,
+                          radamw_index_type ids_type, int64_t n, int64_t rows, int64_t dim, double scale,
+                          int64_t padding_id, int32_t accumulate, void *table_grad, radamw_dtype table_dtype,
+                          int64_t table_stride, void *workspace, int64_t workspace_bytes, radamw_stream_t stream);
+
+/*
+ * Clipped policy loss with a KL term, over n token rows of logits:
+ *   logp_i  = logits[i, labels[i]] - log sum_j exp(logits[i, j])
+ *   r_i     = exp(logp_i - old_logp_i)
+ *   loss_i  = -min(r_i A_i, min(max(r_i, 1 - clip_low), 1 + clip_high) A_i)
+ *             + kl_coef * (exp(ref_logp_i - logp_i) - (ref_logp_i - logp_i) - 1)
+ *   total   = sum of weights_i * loss_i
+ *   grad    = grad_scale * d total / d logits
+ * The gradient passes where A_i >= 0 ? r_i <= 1 + clip_high : r_i >= 1 -
+ * clip_low.  A row takes no part when its label is outside 0 .. vocab-1 or
+ * its weight is 0: its logits are not read (they may hold anything), its
+ * loss and logp are 0 and its gradient is a row of zeros.
+ *   logits     : [n, vocab] of dtype, row stride `stride`.
+ *   old_logp   : n FP32, or NULL: the row's own logp (r_i = 1).
+ *   ref_logp   : n FP32; required when kl_coef != 0, else not read.
+ *   advantages : n FP32.     weights : n FP32, or NULL: all 1.
+ *   opts       : host; 0 <= clip_low <= 1, clip_high >= 0, kl_coef >= 0,
+ *                finite.
+ *   total      : 1 FP32.     loss, logp : n FP32.
+ *   row_stats  : 4 n FP32, 16-byte aligned, the records radamw_logits_grad
+ *                reads; or NULL.
+ *   grad       : [n, vocab] of dtype, row stride grad_stride; NULL for the
+ *                loss alone.  May be exactly the logits (same pointer and
+ *                stride), which it then replaces.
+ * Everything per row is formed in FP64 from the row's maximum and its sum of
+ * exponentials (FP32 by lane, joined in FP64).  Where the gradient is asked
+ * for, the logits of rows up to 256 KiB are read once.
+ */
+typedef struct {
+    double clip_low;
+    double clip_high;
+    double kl_coef;
+} radamw_policy_options;
+/* clip 0.2 on both sides, no KL term. */
+radamw_policy_options radamw_policy_options_default(void);
+int radamw_policy_loss(const void *logits, radamw_dtype dtype, int64_t n, int64_t vocab, int64_t stride,
+                       const void *labels, radamw_index_type labels_type, const float *old_logp, const float *ref_logp,
+                       const float *advantages, const float *weights, const radamw_policy_options *opts,
+                       double grad_scale, float *total, float *loss, float *logp, float *row_stats, void *grad,
+                       int64_t grad_stride, radamw_stream_t stream);
+
+/*
+ * Preference loss of `pairs` pairs of sequences, packed along the rows:
+ * sequence s holds rows offsets[s] .. offsets[s + 1] - 1; sequence p is pair
+ * p's chosen one and sequence pairs + p its rejected one.
+ *   S_s    = sum of logp_i over the rows of s whose label is inside
+ *            0 .. vocab-1 (prompt rows carry a label outside)
+ *   h_p    = beta * ((S_p - ref_logp_p) - (S_(pairs+p) - ref_logp_(pairs+p)))
+ *   loss_p = -(1 - label_smoothing) log sigmoid(h_p)
+ *            - label_smoothing log sigmoid(-h_p)
+ *   total  = sum of weights_p * loss_p
+ *   grad   = grad_scale * d total / d logits
+ * Rows whose label is outside take no part (as in radamw_policy_loss), nor do
+ * rows outside every sequence (their logp is still computed; their gradient
+ * is zeros).  A pair of weight 0 adds nothing to the total and has a zero
+ * gradient.
+ *   offsets   : 2 * pairs + 1 indices of index_type, non-decreasing, within
+ *               0 .. n (read on the device; other values are clamped to that
+ *               range for every access, but the result is unspecified).
+ *   ref_logp  : 2 * pairs FP32, the reference model's S_s.
+ *   weights   : pairs FP32, or NULL: all 1.
+ *   opts      : host; beta >= 0 finite, 0 <= label_smoothing <= 1.
+ *   total     : 1 FP32.  loss : pairs FP32.  seq_logp : 2 * pairs FP32 (S_s).
+ *   logp      : n FP32.  row_stats : 4 n FP32, 16-byte aligned; required.
+ *   logits, labels, grad, strides : as in radamw_policy_loss.
+ * pairs >= 1.  S_s is summed in FP64 from unrounded logp.
+ */
+typedef struct {
+    double beta;
+    double label_smoothing;
+} radamw_preference_options;
+/* beta 0.1, no label smoothing. */
+radamw_preference_options radamw_preference_options_default(void);
+int radamw_preference_loss(const void *logits, radamw_dtype dtype, int64_t n, int64_t vocab, int64_t stride,
+                           const void *labels, radamw_index_type index_type, const void *offsets, int64_t pairs,
+                           const float *ref_logp, const float *weights, const radamw_preference_options *opts,
+                           double grad_scale, float *total, float *loss, float *seq_logp, float *logp,
+                           float *row_stats, void *grad, int64_t grad_stride, radamw_stream_t stream);
+
+/*
+ * The logits' gradient of either loss from the records its forward call
+ * left, for a backward pass that learns its scale only then:
+ *   grad[i, j] = upstream * grad_scale * coef_i * (1[j = labels_i] - p_ij)
+ *   row_stats : 4 n FP32 {max, 1 / sum of exponentials, coef, 1 - p_label}.
+ *   upstream  : 1 FP32 on the device, or NULL: 1.
+ * logits and labels are those of the forward call, unchanged.  grad may be
+ * exactly the logits.
+ */
+int radamw_logits_grad(const void *logits, radamw_dtype dtype, int64_t n, int64_t vocab, int64_t stride,
+                       const void *labels, radamw_index_type labels_type, const float *row_stats,
+                       const float *upstream, double grad_scale, void *grad, int64_t grad_stride,
+                       radamw_stream_t stream);
+
 /* Utilities. */
 const char *radamw_status_string(int status);
 /* Last HIP error code seen by this thread inside the library (0 = none). */

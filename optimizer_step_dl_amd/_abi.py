@@ -27,6 +27,7 @@ LIB_PATH = os.path.join(_HERE, "libradamw.so")
 RADAMW_OK = 0
 F32, F16, BF16 = 0, 1, 2
 _DTYPE_CODE = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+_INDEX_CODE = {torch.int32: 0, torch.int64: 1}
 
 
 class RadamwError(RuntimeError):
@@ -76,6 +77,14 @@ class _Segment(ctypes.Structure):
                 ("n", ctypes.c_int64)]
 
 
+class PolicyOptions(ctypes.Structure):
+    _fields_ = [("clip_low", ctypes.c_double), ("clip_high", ctypes.c_double), ("kl_coef", ctypes.c_double)]
+
+
+class PreferenceOptions(ctypes.Structure):
+    _fields_ = [("beta", ctypes.c_double), ("label_smoothing", ctypes.c_double)]
+
+
 class Stats(ctypes.Structure):
     _fields_ = [("w", ctypes.c_uint32 * 3)]
 
@@ -99,6 +108,14 @@ class FusedResult(ctypes.Structure):
 def options(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-5, weight_decay=1e-4, amsgrad=False,
             maximize=False) -> Options:
     return Options(lr, beta1, beta2, eps, weight_decay, int(amsgrad), int(maximize))
+
+
+def policy_options(clip_low=0.2, clip_high=0.2, kl_coef=0.0) -> PolicyOptions:
+    return PolicyOptions(float(clip_low), float(clip_high), float(kl_coef))
+
+
+def preference_options(beta=0.1, label_smoothing=0.0) -> PreferenceOptions:
+    return PreferenceOptions(float(beta), float(label_smoothing))
 
 
 def control(gradient_scale=1.0, skip_update=False) -> Control:
@@ -178,6 +195,17 @@ def load(path: str = LIB_PATH):
         "radamw_list_destroy": ([vp], ctypes.c_int),
         "radamw_lists_fused_step": ([P(vp), i32, P(u64), P(Options), dbl, dbl, i32, vp, P(FusedResult)],
                                     ctypes.c_int),
+        "radamw_embedding_lookup": ([vp, i32, i64, i64, i64, vp, i32, i64, dbl, vp, i32, i64, vp], ctypes.c_int),
+        "radamw_embedding_grad_workspace_bytes": ([i64, i64, i64], i64),
+        "radamw_embedding_grad": ([vp, i32, i64, vp, i32, i64, i64, i64, dbl, i64, i32, vp, i32, i64, vp, i64, vp],
+                                  ctypes.c_int),
+        "radamw_policy_options_default": ([], PolicyOptions),
+        "radamw_policy_loss": ([vp, i32, i64, i64, i64, vp, i32, vp, vp, vp, vp, P(PolicyOptions), dbl, vp, vp, vp, vp,
+                                vp, i64, vp], ctypes.c_int),
+        "radamw_preference_options_default": ([], PreferenceOptions),
+        "radamw_preference_loss": ([vp, i32, i64, i64, i64, vp, i32, vp, i64, vp, vp, P(PreferenceOptions), dbl, vp, vp,
+                                    vp, vp, vp, vp, i64, vp], ctypes.c_int),
+        "radamw_logits_grad": ([vp, i32, i64, i64, i64, vp, i32, vp, vp, dbl, vp, i64, vp], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -194,7 +222,9 @@ EXPORTS = ("radamw_options_default", "radamw_step", "radamw_step_inplace", "rada
            "radamw_fused_step_multi", "radamw_fused_step_multi_noalloc", "radamw_host_coefficients", "radamw_status_string",
            "radamw_last_hip_error", "radamw_launch_count", "radamw_time_next_update",
            "radamw_list_create", "radamw_list_step", "radamw_list_fused_step", "radamw_list_destroy",
-           "radamw_lists_fused_step")
+           "radamw_lists_fused_step", "radamw_embedding_lookup", "radamw_embedding_grad_workspace_bytes",
+           "radamw_embedding_grad", "radamw_policy_options_default", "radamw_policy_loss",
+           "radamw_preference_options_default", "radamw_preference_loss", "radamw_logits_grad")
 
 
 # ----------------------------------------------------------------- helpers --
@@ -740,6 +770,192 @@ def radamw_lists_fused_step(lists: Sequence[TensorList], steps: Sequence[int], o
         raise DecisionMismatch("radamw_lists_fused_step", res, steps=[int(x) for x in st])
     _check(rc, "radamw_lists_fused_step")
     return res, [int(x) for x in st]
+
+
+# ------------------------------------------------------ vocabulary operators --
+
+def _rows2d(t: torch.Tensor, what: str, device, n=None, width=None) -> int:
+    """Check a [n, width] device tensor with unit column stride; its row
+    stride in elements."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{what} must be a device tensor")
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, expected {device}")
+    if t.dim() != 2:
+        raise ValueError(f"{what} must have two dimensions (got {t.dim()})")
+    if t.dtype not in _DTYPE_CODE:
+        raise ValueError(f"{what} dtype {t.dtype} is not float32/float16/bfloat16")
+    rows, cols = t.shape
+    if (n is not None and rows != n) or (width is not None and cols != width):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {(n, width)}")
+    row, col = t.stride()
+    if rows <= 1:  # one row (or none): its stride is never used
+        row = max(row, cols)
+    if (cols > 1 and col != 1) or row < cols:
+        raise ValueError(f"{what} must have unit column stride and rows that do not overlap (strides {t.stride()})")
+    return row
+
+
+def _index(t: torch.Tensor, what: str, n: int, device) -> int:
+    """Check a contiguous index tensor of n entries; its type code."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{what} must be a device tensor")
+    if t.dtype not in _INDEX_CODE:
+        raise ValueError(f"{what} dtype {t.dtype} is not int32/int64")
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, expected {device}")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous with {n} entries (got {t.numel()})")
+    return _INDEX_CODE[t.dtype]
+
+
+def _row_values(t: Optional[torch.Tensor], what: str, n: int, dev_index: int):
+    """Pointer of a contiguous FP32 tensor of n values, or None."""
+    if t is None:
+        return None
+    _check_fast(t, what, dev_index, n, torch.float32)
+    return t.data_ptr()
+
+
+def radamw_embedding_lookup(table: torch.Tensor, ids: torch.Tensor, out: torch.Tensor, scale: float = 1.0) -> None:
+    """out[t] = scale * table[ids[t]] for table [rows, dim], ids of any shape
+    (int32 / int64, contiguous) and out [ids.numel(), dim]; zeros where an
+    id is outside the table."""
+    lib = load()
+    dev = table.device
+    ts = _rows2d(table, "table", dev)
+    rows, dim = table.shape
+    n = ids.numel()
+    idt = _index(ids, "ids", n, dev)
+    os_ = _rows2d(out, "out", dev, n, dim)
+    with torch.cuda.device(dev):
+        rc = lib.radamw_embedding_lookup(table.data_ptr(), _DTYPE_CODE[table.dtype], rows, dim, ts, ids.data_ptr(), idt,
+                                         n, float(scale), out.data_ptr(), _DTYPE_CODE[out.dtype], os_, _stream(dev))
+    _check(rc, "radamw_embedding_lookup")
+
+
+def radamw_embedding_grad_workspace_bytes(n: int, rows: int, dim: int) -> int:
+    r = load().radamw_embedding_grad_workspace_bytes(n, rows, dim)
+    if r < 0:
+        raise RadamwError(int(r), "radamw_embedding_grad_workspace_bytes")
+    return int(r)
+
+
+def radamw_embedding_grad(grad_out: torch.Tensor, ids: torch.Tensor, table_grad: torch.Tensor,
+                          workspace: torch.Tensor, scale: float = 1.0, padding_id: Optional[int] = None,
+                          accumulate: bool = False) -> None:
+    """table_grad (+)= the lookup's gradient: every row, or with
+    ``accumulate`` only the rows some token names.  grad_out is
+    [ids.numel(), dim], table_grad [rows, dim]; ``workspace`` holds at least
+    radamw_embedding_grad_workspace_bytes(ids.numel(), rows, dim) bytes."""
+    lib = load()
+    dev = table_grad.device
+    ts = _rows2d(table_grad, "table_grad", dev)
+    rows, dim = table_grad.shape
+    n = ids.numel()
+    idt = _index(ids, "ids", n, dev)
+    gs = _rows2d(grad_out, "grad_out", dev, n, dim)
+    _dense(workspace, "workspace", device=dev)
+    with torch.cuda.device(dev):
+        rc = lib.radamw_embedding_grad(grad_out.data_ptr(), _DTYPE_CODE[grad_out.dtype], gs, ids.data_ptr(), idt, n,
+                                       rows, dim, float(scale), -1 if padding_id is None else int(padding_id),
+                                       int(bool(accumulate)), table_grad.data_ptr(), _DTYPE_CODE[table_grad.dtype], ts,
+                                       workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(dev))
+    _check(rc, "radamw_embedding_grad")
+
+
+def radamw_policy_options_default() -> PolicyOptions:
+    return load().radamw_policy_options_default()
+
+
+def radamw_preference_options_default() -> PreferenceOptions:
+    return load().radamw_preference_options_default()
+
+
+def _logits(logits, labels, grad):
+    """(device, n, vocab, row stride, labels' type code, gradient pointer and
+    row stride) of a loss's logits, labels and optional gradient."""
+    dev = logits.device
+    st = _rows2d(logits, "logits", dev)
+    n, vocab = logits.shape
+    idt = _index(labels, "labels", n, dev)
+    if grad is None:
+        return dev, n, vocab, st, idt, None, 0
+    gs = _rows2d(grad, "grad", dev, n, vocab)
+    if grad.dtype != logits.dtype:
+        raise ValueError(f"grad must be {logits.dtype} (got {grad.dtype})")
+    return dev, n, vocab, st, idt, grad.data_ptr(), gs
+
+
+def radamw_policy_loss(logits: torch.Tensor, labels: torch.Tensor, old_logp: Optional[torch.Tensor],
+                       advantages: torch.Tensor, opts: PolicyOptions, total: torch.Tensor, loss: torch.Tensor,
+                       logp: torch.Tensor, *, ref_logp: Optional[torch.Tensor] = None,
+                       weights: Optional[torch.Tensor] = None, row_stats: Optional[torch.Tensor] = None,
+                       grad: Optional[torch.Tensor] = None, grad_scale: float = 1.0) -> None:
+    """Clipped policy loss of the rows of logits [n, vocab]: writes total
+    (1), loss and logp (n), row_stats (n x 4, when given) and, when ``grad``
+    is given, grad_scale * d total / d logits (``grad`` may be ``logits``)."""
+    lib = load()
+    dev, n, vocab, st, idt, gp, gs = _logits(logits, labels, grad)
+    di = dev.index
+    old = _row_values(old_logp, "old_logp", n, di)
+    ref = _row_values(ref_logp, "ref_logp", n, di)
+    adv = _row_values(advantages, "advantages", n, di)
+    wts = _row_values(weights, "weights", n, di)
+    tot = _row_values(total, "total", 1, di)
+    los = _row_values(loss, "loss", n, di)
+    lgp = _row_values(logp, "logp", n, di)
+    sta = _row_values(row_stats, "row_stats", 4 * n, di)
+    with torch.cuda.device(dev):
+        rc = lib.radamw_policy_loss(logits.data_ptr(), _DTYPE_CODE[logits.dtype], n, vocab, st, labels.data_ptr(), idt,
+                                    old, ref, adv, wts, ctypes.byref(opts), float(grad_scale), tot, los, lgp, sta, gp,
+                                    gs, _stream(dev))
+    _check(rc, "radamw_policy_loss")
+
+
+def radamw_preference_loss(logits: torch.Tensor, labels: torch.Tensor, offsets: torch.Tensor, ref_logp: torch.Tensor,
+                           opts: PreferenceOptions, total: torch.Tensor, loss: torch.Tensor, seq_logp: torch.Tensor,
+                           logp: torch.Tensor, row_stats: torch.Tensor, *, weights: Optional[torch.Tensor] = None,
+                           grad: Optional[torch.Tensor] = None, grad_scale: float = 1.0) -> None:
+    """Preference loss of pairs of sequences packed along the rows of logits
+    [n, vocab]; offsets (2 * pairs + 1, the labels' dtype) give the rows of
+    the chosen sequences, then of the rejected ones.  Writes total (1), loss
+    (pairs), seq_logp (2 * pairs), logp (n), row_stats (n x 4) and, when
+    ``grad`` is given, grad_scale * d total / d logits."""
+    lib = load()
+    dev, n, vocab, st, idt, gp, gs = _logits(logits, labels, grad)
+    di = dev.index
+    pairs = loss.numel()
+    if _index(offsets, "offsets", 2 * pairs + 1, dev) != idt:
+        raise ValueError(f"offsets must be {labels.dtype}, as the labels (got {offsets.dtype})")
+    ref = _row_values(ref_logp, "ref_logp", 2 * pairs, di)
+    wts = _row_values(weights, "weights", pairs, di)
+    tot = _row_values(total, "total", 1, di)
+    los = _row_values(loss, "loss", pairs, di)
+    seq = _row_values(seq_logp, "seq_logp", 2 * pairs, di)
+    lgp = _row_values(logp, "logp", n, di)
+    sta = _row_values(row_stats, "row_stats", 4 * n, di)
+    with torch.cuda.device(dev):
+        rc = lib.radamw_preference_loss(logits.data_ptr(), _DTYPE_CODE[logits.dtype], n, vocab, st, labels.data_ptr(),
+                                        idt, offsets.data_ptr(), pairs, ref, wts, ctypes.byref(opts), float(grad_scale),
+                                        tot, los, seq, lgp, sta, gp, gs, _stream(dev))
+    _check(rc, "radamw_preference_loss")
+
+
+def radamw_logits_grad(logits: torch.Tensor, labels: torch.Tensor, row_stats: torch.Tensor, grad: torch.Tensor,
+                       upstream: Optional[torch.Tensor] = None, grad_scale: float = 1.0) -> None:
+    """grad = upstream * grad_scale * the gradient either loss's records
+    (row_stats) stand for; upstream is one FP32 value on the device."""
+    lib = load()
+    if grad is None:
+        raise ValueError("grad must be a device tensor")
+    dev, n, vocab, st, idt, gp, gs = _logits(logits, labels, grad)
+    sta = _row_values(row_stats, "row_stats", 4 * n, dev.index)
+    ups = _row_values(upstream, "upstream", 1, dev.index)
+    with torch.cuda.device(dev):
+        rc = lib.radamw_logits_grad(logits.data_ptr(), _DTYPE_CODE[logits.dtype], n, vocab, st, labels.data_ptr(), idt,
+                                    sta, ups, float(grad_scale), gp, gs, _stream(dev))
+    _check(rc, "radamw_logits_grad")
 
 
 def radamw_host_coefficients(opts: Options, t: int, gradient_scale: float = 1.0) -> list[float]:

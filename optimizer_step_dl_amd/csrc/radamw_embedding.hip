@@ -1,0 +1,711 @@
+// radamw_embedding.hip -- the embedding lookup and its gradient for gfx950.
+//
+//   lookup    out[t, :] = scale * table[id_t, :]
+//   gradient  dW[v, :] (+)= scale * sum over t with id_t = v of dY[t, :]
+//
+// Both only move rows: one product or one sum per value read, so they are
+// bound by HBM and every lane moves eight values (16 or 32 bytes) at a time.
+//
+// The gradient sums in a fixed order, without atomics on values: the token
+// positions are sorted by id (a stable radix sort), the sorted list is cut
+// into chunks of equal length, and each chunk is summed by waves that own
+// 64 x 8 columns.  A run of equal ids inside one chunk is finished there; a
+// run that crosses chunks leaves FP32 partial sums, which a second launch
+// joins in the order of the chunks.  Equal chunks keep the waves balanced
+// however uneven the ids are.
+#include "radamw_rows.h"
+#include "radamw_vocab.h"
+
+namespace radamw {
+
+namespace {
+
+constexpr int ROW_BLOCK = 256;
+
+int log2_ceil(int64_t v) {
+    int b = 0;
+    while ((int64_t(1) << b) < v) ++b;
+    return b;
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------- lookup --
+
+constexpr int LOOKUP_UNROLL = 2;
+
+// x * scale as an FP32 value: the empty asm keeps the compiler from fusing
+// the product with a conversion to FP16, which would round the exact product
+// in some places and its FP32 value in others.
+__device__ __forceinline__ float scaled(float x, float scale) {
+    float p = x * scale;
+    asm("" : "+v"(p));
+    return p;
+}
+
+// A group of 2^lg lanes serves one row's 8-value pieces piece, piece + 2^lg
+// of the column tile blockIdx.y.
+template <int TDT, int ODT>
+__global__ __launch_bounds__(ROW_BLOCK) void embedding_lookup(LookupArgs a, int lg) {
+    const int lanes = 1 << lg;
+    const int64_t t = (int64_t(blockIdx.x) << (8 - lg)) + (threadIdx.x >> lg);
+    if (t >= a.n) return;
+    const int64_t id = load_index(a.ids, a.wide_ids, t);
+    const bool inside = id >= 0 && id < a.rows;
+    const char *src = static_cast<const char *>(a.table) + (inside ? id : 0) * a.table_stride * elem_bytes<TDT>;
+    char *dst = static_cast<char *>(a.out) + t * a.out_stride * elem_bytes<ODT>;
+    const int64_t first = int64_t(blockIdx.y) * LOOKUP_UNROLL * lanes + (threadIdx.x & (lanes - 1));
+    Raw8<TDT> r[LOOKUP_UNROLL];
+#pragma unroll
+    for (int u = 0; u < LOOKUP_UNROLL; ++u) {
+        const int64_t e = (first + u * lanes) * 8;
+        if (inside && e + 8 <= a.dim) r[u] = load_raw8<TDT>(src, e);
+    }
+#pragma unroll
+    for (int u = 0; u < LOOKUP_UNROLL; ++u) {
+        const int64_t e = (first + u * lanes) * 8;
+        if (e + 8 <= a.dim) {
+            f32x8 v;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = inside ? scaled(raw_value<TDT>(r[u], j), a.scale) : 0.0f;
+            store8<ODT>(dst, e, v);
+        } else if (e < a.dim) {
+            for (int64_t k = e; k < a.dim; ++k)
+                store_value<ODT>(dst, k, inside ? scaled(load_value<TDT>(src, k), a.scale) : 0.0f);
+        }
+    }
+}
+
+int lookup_lanes_log2(int64_t dim) {
+    const int64_t pieces = (dim + 7) / 8;
+    const int lg = log2_ceil((pieces + LOOKUP_UNROLL - 1) / LOOKUP_UNROLL);
+    return lg < 3 ? 3 : lg > 8 ? 8 : lg;
+}
+
+int64_t lookup_blocks(int64_t n, int64_t dim) {
+    const int lg = lookup_lanes_log2(dim);
+    return (n + (int64_t(1) << (8 - lg)) - 1) >> (8 - lg);
+}
+
+template <int TDT>
+static hipError_t lookup_out(const LookupArgs &a, int odt, hipStream_t stream) {
+    const int lg = lookup_lanes_log2(a.dim);
+    const int64_t pieces = (a.dim + 7) / 8, tile = int64_t(LOOKUP_UNROLL) << lg;
+    const dim3 grid(static_cast<unsigned>(lookup_blocks(a.n, a.dim)),
+                    static_cast<unsigned>((pieces + tile - 1) / tile));
+    switch (odt) {
+    case G_F32: hipLaunchKernelGGL((embedding_lookup<TDT, G_F32>), grid, dim3(ROW_BLOCK), 0, stream, a, lg); break;
+    case G_F16: hipLaunchKernelGGL((embedding_lookup<TDT, G_F16>), grid, dim3(ROW_BLOCK), 0, stream, a, lg); break;
+    default: hipLaunchKernelGGL((embedding_lookup<TDT, G_BF16>), grid, dim3(ROW_BLOCK), 0, stream, a, lg); break;
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_embedding_lookup(const LookupArgs &a, int tdt, int odt, hipStream_t stream) {
+    switch (tdt) {
+    case G_F32: return lookup_out<G_F32>(a, odt, stream);
+    case G_F16: return lookup_out<G_F16>(a, odt, stream);
+    default: return lookup_out<G_BF16>(a, odt, stream);
+    }
+}
+
+// ------------------------------------------------------------------ sort --
+//
+// Least-significant-digit radix sort of (id, position), stable, so that
+// equal ids keep the order of their tokens.  An id that takes no part
+// (outside the table, or the padding id) gets the key `rows` and sorts last.
+// Digits have up to 10 bits: two passes for vocabularies below 2^20.
+
+struct SortKeys {
+    const void *ids;  // pass 0 reads the ids, later passes keys / pos
+    const uint32_t *keys;
+    const uint32_t *pos;
+    int64_t n, rows, padding_id;
+    int32_t wide_ids;
+};
+
+__device__ __forceinline__ uint32_t token_key(const SortKeys &s, int64_t i) {
+    const int64_t id = load_index(s.ids, s.wide_ids, i);
+    return static_cast<uint32_t>(id >= 0 && id < s.rows && id != s.padding_id ? id : s.rows);
+}
+
+// Among the lanes of a wave with `in` set: how many before this one have the
+// same digit, and how many have it at all.
+__device__ __forceinline__ void match_digit(uint32_t digit, int bits, bool in, int *before, int *total) {
+    uint64_t same = __ballot(in);
+    for (int b = 0; b < bits; ++b) {
+        const bool set = (digit >> b) & 1;
+        const uint64_t bal = __ballot(set);
+        same &= set ? bal : ~bal;
+    }
+    const uint64_t lower = (uint64_t(1) << (threadIdx.x & 63)) - 1;
+    *before = __popcll(same & lower);
+    *total = __popcll(same);
+}
+
+// Inclusive sum over the lanes of a wave.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const uint32_t u = __shfl_up(v, off, 64);
+        if (lane >= off) v += u;
+    }
+    return v;
+}
+
+// Exclusive sum over a workgroup of WAVES waves; *all receives the total.
+// `part` is LDS of WAVES words; ends with every lane past its last read.
+template <int WAVES>
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *part, uint32_t *all) {
+    const uint32_t inc = wave_scan(v);
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 63) part[wave] = inc;
+    __syncthreads();
+    uint32_t base = 0, sum = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+        const uint32_t p = part[w];
+        base += w < wave ? p : 0;
+        sum += p;
+    }
+    *all = sum;
+    __syncthreads();
+    return base + inc - v;
+}
+
+// One pass's place of every key of a workgroup: waves own consecutive parts
+// of the keys and walk them 64 at a time; hist[wave][digit] counts the keys
+// of a wave seen so far, then holds the wave's first place for the digit.
+template <int WAVES, int ROUNDS>
+struct Ranker {
+    uint32_t digit[ROUNDS];
+    int32_t rank[ROUNDS];  // among the wave's keys of that digit
+
+    __device__ __forceinline__ void count(const uint32_t (&key)[ROUNDS], int rounds, int64_t first, int64_t n, int shift,
+                                          int bits, uint32_t *hist, int bins) {
+        for (int i = threadIdx.x; i < WAVES * bins; i += WAVES * 64) hist[i] = 0;
+        __syncthreads();
+        uint32_t *mine = hist + (threadIdx.x >> 6) * bins;
+#pragma unroll
+        for (int r = 0; r < ROUNDS; ++r) {
+            if (r >= rounds) break;
+            const bool in = first + r * 64 < n;
+            digit[r] = (key[r] >> shift) & (bins - 1);
+            int before, total;
+            match_digit(digit[r], bits, in, &before, &total);
+            const uint32_t seen = in ? mine[digit[r]] : 0;
+            rank[r] = static_cast<int>(seen) + before;
+            // every lane has read before the last of its equals adds them
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            if (in && before + 1 == total) mine[digit[r]] = seen + total;
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        }
+        __syncthreads();
+    }
+};
+
+constexpr int SORT_SMALL_BLOCK = 1024;
+constexpr int SORT_SMALL_WAVES = SORT_SMALL_BLOCK / 64;
+constexpr int SORT_SMALL_ROUNDS = int(SORT_SMALL_MAX / SORT_SMALL_BLOCK);
+constexpr int SORT_SMALL_BITS = 9;
+
+// Clear the presence bits of table rows; part `part` of `parts`.
+__device__ __forceinline__ void clear_bits(uint32_t *present, int64_t rows, int64_t part, int64_t parts, int block) {
+    const int64_t words = (rows + 31) / 32;
+    for (int64_t i = part * block + threadIdx.x; i < words; i += parts * block) present[i] = 0;
+}
+
+// The whole sort of up to SORT_SMALL_MAX tokens by one workgroup: the keys
+// stay in LDS between the passes.
+__global__ __launch_bounds__(SORT_SMALL_BLOCK) void sort_small(SortKeys s, int bits, int passes, uint32_t *keys_out,
+                                                               uint32_t *pos_out, uint32_t *present) {
+    __shared__ uint32_t lkey[SORT_SMALL_MAX];
+    __shared__ uint16_t lpos[SORT_SMALL_MAX];
+    __shared__ uint32_t hist[SORT_SMALL_WAVES << SORT_SMALL_BITS];
+    __shared__ uint32_t part[SORT_SMALL_WAVES];
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const int rounds = static_cast<int>((s.n + SORT_SMALL_BLOCK - 1) / SORT_SMALL_BLOCK);
+    const int64_t first = int64_t(wave) * rounds * 64 + lane;
+    if (present) {
+        clear_bits(present, s.rows, 0, 1, SORT_SMALL_BLOCK);
+        __threadfence();  // the bits set at the end land on cleared words
+    }
+    uint32_t key[SORT_SMALL_ROUNDS];
+    uint32_t pos[SORT_SMALL_ROUNDS];
+#pragma unroll
+    for (int r = 0; r < SORT_SMALL_ROUNDS; ++r) {
+        const int64_t i = first + r * 64;
+        key[r] = r < rounds && i < s.n ? token_key(s, i) : 0;
+        pos[r] = static_cast<uint32_t>(i);
+    }
+    const int bins = 1 << bits;
+    Ranker<SORT_SMALL_WAVES, SORT_SMALL_ROUNDS> rk;
+    for (int pass = 0; pass < passes; ++pass) {
+        rk.count(key, rounds, first, s.n, pass * bits, bits, hist, bins);
+        // thread b: digit b's keys over the waves, then over the digits
+        uint32_t mine = 0;
+        if (tid < bins)
+            for (int w = 0; w < SORT_SMALL_WAVES; ++w) {
+                const uint32_t c = hist[w * bins + tid];
+                hist[w * bins + tid] = mine;
+                mine += c;
+            }
+        uint32_t all;
+        const uint32_t base = block_scan<SORT_SMALL_WAVES>(mine, part, &all);
+        if (tid < bins)
+            for (int w = 0; w < SORT_SMALL_WAVES; ++w) hist[w * bins + tid] += base;
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < SORT_SMALL_ROUNDS; ++r) {
+            if (r < rounds && first + r * 64 < s.n) {
+                const uint32_t at = hist[wave * bins + rk.digit[r]] + rk.rank[r];
+                lkey[at] = key[r];
+                lpos[at] = static_cast<uint16_t>(pos[r]);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < SORT_SMALL_ROUNDS; ++r) {
+            if (r < rounds && first + r * 64 < s.n) {
+                key[r] = lkey[first + r * 64];
+                pos[r] = lpos[first + r * 64];
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < SORT_SMALL_ROUNDS; ++r) {
+        const int64_t i = first + r * 64;
+        if (r >= rounds || i >= s.n) continue;
+        keys_out[i] = key[r];
+        pos_out[i] = pos[r];
+        if (present && key[r] < static_cast<uint32_t>(s.rows) && (i == 0 || lkey[i - 1] != key[r]))
+            atomicOr(present + (key[r] >> 5), 1u << (key[r] & 31));
+    }
+}
+
+constexpr int SORT_BLOCK = 512;
+constexpr int SORT_WAVES = SORT_BLOCK / 64;
+constexpr int SORT_ROUNDS = int(SORT_TILE / SORT_BLOCK);
+constexpr int SORT_MAX_BINS = 1 << SORT_MAX_DIGIT_BITS;
+
+// Digit counts of tile blockIdx.x, as counts[digit * tiles + tile], so that
+// one exclusive sum over the array gives each tile its places.
+template <bool FIRST>
+__global__ __launch_bounds__(SORT_BLOCK) void radix_count(SortKeys s, int shift, int bits, uint32_t *counts,
+                                                          uint32_t *present) {
+    __shared__ uint32_t hist[SORT_MAX_BINS];
+    const int bins = 1 << bits;
+    for (int i = threadIdx.x; i < bins; i += SORT_BLOCK) hist[i] = 0;
+    if (FIRST && present) clear_bits(present, s.rows, blockIdx.x, gridDim.x, SORT_BLOCK);
+    __syncthreads();
+    const int64_t begin = int64_t(blockIdx.x) * SORT_TILE;
+    for (int r = 0; r < SORT_ROUNDS; ++r) {
+        const int64_t i = begin + r * SORT_BLOCK + threadIdx.x;
+        if (i < s.n) {
+            const uint32_t key = FIRST ? token_key(s, i) : s.keys[i];
+            atomicAdd(&hist[(key >> shift) & (bins - 1)], 1u);
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < bins; i += SORT_BLOCK) counts[int64_t(i) * gridDim.x + blockIdx.x] = hist[i];
+}
+
+constexpr int SCAN_BLOCK = 1024;
+
+// Exclusive sum over m counts in place, by one workgroup.
+__global__ __launch_bounds__(SCAN_BLOCK) void radix_scan(uint32_t *counts, int64_t m) {
+    __shared__ uint32_t part[SCAN_BLOCK / 64];
+    uint32_t carry = 0;
+    for (int64_t base = 0; base < m; base += SCAN_BLOCK * 4) {
+        const int64_t i = base + int64_t(threadIdx.x) * 4;
+        uint32_t v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = i + j < m ? counts[i + j] : 0;
+        uint32_t all;
+        uint32_t at = carry + block_scan<SCAN_BLOCK / 64>(v[0] + v[1] + v[2] + v[3], part, &all);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (i + j < m) counts[i + j] = at;
+            at += v[j];
+        }
+        carry += all;
+    }
+}
+
+template <bool FIRST>
+__global__ __launch_bounds__(SORT_BLOCK) void radix_scatter(SortKeys s, int shift, int bits, const uint32_t *counts,
+                                                            uint32_t *keys_out, uint32_t *pos_out) {
+    __shared__ uint32_t hist[SORT_WAVES * SORT_MAX_BINS];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int bins = 1 << bits;
+    const int64_t first = int64_t(blockIdx.x) * SORT_TILE + int64_t(wave) * SORT_ROUNDS * 64 + lane;
+    uint32_t key[SORT_ROUNDS], pos[SORT_ROUNDS];
+#pragma unroll
+    for (int r = 0; r < SORT_ROUNDS; ++r) {
+        const int64_t i = first + r * 64;
+        key[r] = i < s.n ? (FIRST ? token_key(s, i) : s.keys[i]) : 0;
+        pos[r] = i < s.n ? (FIRST ? static_cast<uint32_t>(i) : s.pos[i]) : 0;
+    }
+    Ranker<SORT_WAVES, SORT_ROUNDS> rk;
+    rk.count(key, SORT_ROUNDS, first, s.n, shift, bits, hist, bins);
+    for (int b = threadIdx.x; b < bins; b += SORT_BLOCK) {
+        uint32_t at = counts[int64_t(b) * gridDim.x + blockIdx.x];
+        for (int w = 0; w < SORT_WAVES; ++w) {
+            const uint32_t c = hist[w * bins + b];
+            hist[w * bins + b] = at;
+            at += c;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < SORT_ROUNDS; ++r) {
+        if (first + r * 64 < s.n) {
+            const uint32_t at = hist[wave * bins + rk.digit[r]] + rk.rank[r];
+            keys_out[at] = key[r];
+            pos_out[at] = pos[r];
+        }
+    }
+}
+
+// Set the presence bit of every key of a sorted list.
+__global__ __launch_bounds__(256) void mark_present(const uint32_t *keys, int64_t n, int64_t rows, uint32_t *present) {
+    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= n) return;
+    const uint32_t key = keys[i];
+    if (key < static_cast<uint32_t>(rows) && (i == 0 || keys[i - 1] != key))
+        atomicOr(present + (key >> 5), 1u << (key & 31));
+}
+
+// -------------------------------------------------------------- gradient --
+
+struct SumArgs {
+    const void *grad_out;
+    void *table_grad;
+    const uint32_t *keys, *pos;
+    const uint32_t *present;
+    float *partials;
+    int64_t grad_stride, table_stride, n, rows, dim, chunks;
+    int32_t chunk, tiles;  // tokens per chunk; column tiles per row
+    int32_t accumulate;
+    float scale;
+    int64_t sum_blocks;  // workgroups below this sum, the others clear absent rows
+    int64_t rows_per_block;
+};
+
+// v into columns [e, e + 8) of table row `key`, rounded once.
+template <int TDT, bool ACC>
+__device__ __forceinline__ void write_row(const SumArgs &a, uint32_t key, int64_t e, f32x8 v) {
+    char *dst = static_cast<char *>(a.table_grad) + int64_t(key) * a.table_stride * elem_bytes<TDT>;
+    if (e + 8 <= a.dim) {
+        if constexpr (ACC) {
+            const Raw8<TDT> old = load_raw8<TDT>(dst, e);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = __builtin_fmaf(v[j], a.scale, raw_value<TDT>(old, j));
+        } else {
+            v *= a.scale;
+        }
+        store8<TDT>(dst, e, v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (e + j < a.dim) {
+                const float x = ACC ? __builtin_fmaf(v[j], a.scale, load_value<TDT>(dst, e + j)) : v[j] * a.scale;
+                store_value<TDT>(dst, e + j, x);
+            }
+        }
+    }
+}
+
+constexpr int SUM_UNROLL = 8;  // rows in flight per lane
+
+// Columns [e, e + 8) of one chunk of the sorted tokens.
+template <int GDT, int TDT, bool ACC>
+__device__ __forceinline__ void sum_chunk(const SumArgs &a, int64_t chunk, int64_t e) {
+    const int64_t base = chunk * a.chunk;
+    const int count = static_cast<int>(a.n - base < a.chunk ? a.n - base : a.chunk);
+    const uint32_t *keys = a.keys + base, *pos = a.pos + base;
+    const uint32_t rows = static_cast<uint32_t>(a.rows);
+    const bool whole = e + 8 <= a.dim;
+    bool continued = base > 0 && a.keys[base - 1] == keys[0];  // the first run began in an earlier chunk
+    const bool more = base + count < a.n && a.keys[base + count] == keys[count - 1];
+    f32x8 acc = 0.0f;
+    for (int j0 = 0; j0 < count; j0 += SUM_UNROLL) {
+        uint32_t key[SUM_UNROLL + 1];
+        f32x8 v[SUM_UNROLL];
+        Raw8<GDT> raw[SUM_UNROLL];
+#pragma unroll
+        for (int u = 0; u <= SUM_UNROLL; ++u) key[u] = j0 + u < count ? keys[j0 + u] : 0xffffffffu;
+#pragma unroll
+        for (int u = 0; u < SUM_UNROLL; ++u) {
+            if (key[u] < rows) {
+                const char *src = static_cast<const char *>(a.grad_out) +
+                                  int64_t(pos[j0 + u]) * a.grad_stride * elem_bytes<GDT>;
+                if (whole) {
+                    raw[u] = load_raw8<GDT>(src, e);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[u][k] = e + k < a.dim ? load_value<GDT>(src, e + k) : 0.0f;
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < SUM_UNROLL; ++u) {
+            if (key[u] >= rows) continue;
+            if (whole) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) acc[k] += raw_value<GDT>(raw[u], k);
+            } else {
+                acc += v[u];
+            }
+            if (key[u + 1] != key[u]) {  // the run ends here, or crosses into the next chunk
+                const bool open = j0 + u + 1 == count && more;
+                if (!continued && !open) {
+                    write_row<TDT, ACC>(a, key[u], e, acc);
+                } else {
+                    float *slot = a.partials + (2 * chunk + (continued ? 0 : 1)) * a.dim;
+                    if (whole) {
+                        store8<G_F32>(slot, e, acc);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (e + k < a.dim) slot[e + k] = acc[k];
+                    }
+                }
+                continued = false;
+                acc = 0.0f;
+            }
+        }
+    }
+}
+
+// Rows of the table that no token names: zeros.
+template <int TDT>
+__device__ __forceinline__ void clear_rows(const SumArgs &a, int64_t block, int lg) {
+    const int lanes = 1 << lg;
+    const int64_t begin = block * a.rows_per_block;
+    const int64_t end = begin + a.rows_per_block < a.rows ? begin + a.rows_per_block : a.rows;
+    for (int64_t r = begin + (threadIdx.x >> lg); r < end; r += ROW_BLOCK >> lg) {
+        if ((a.present[r >> 5] >> (r & 31)) & 1) continue;
+        char *dst = static_cast<char *>(a.table_grad) + r * a.table_stride * elem_bytes<TDT>;
+        for (int64_t e = int64_t(threadIdx.x & (lanes - 1)) * 8; e < a.dim; e += lanes * 8) {
+            if (e + 8 <= a.dim) {
+                store8<TDT>(dst, e, f32x8(0.0f));
+            } else {
+                for (int64_t k = e; k < a.dim; ++k) store_value<TDT>(dst, k, 0.0f);
+            }
+        }
+    }
+}
+
+template <int GDT, int TDT, bool ACC>
+__global__ __launch_bounds__(ROW_BLOCK) void embedding_sum(SumArgs a, int lg) {
+    if (!ACC && blockIdx.x >= a.sum_blocks) {
+        clear_rows<TDT>(a, blockIdx.x - a.sum_blocks, lg < 6 ? lg : 8);
+        return;
+    }
+    const int64_t unit = (int64_t(blockIdx.x) << (8 - lg)) + (threadIdx.x >> lg);
+    if (lg == 6) {
+        // a whole wave shares its chunk: ids and positions are scalar loads
+        const uint32_t u = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(unit));
+        const uint32_t chunk = u / a.tiles, tile = u % a.tiles;
+        const int64_t e = (int64_t(tile) * 64 + (threadIdx.x & 63)) * 8;
+        if (chunk < a.chunks && e < a.dim) sum_chunk<GDT, TDT, ACC>(a, chunk, e);
+    } else {
+        const int64_t e = int64_t(threadIdx.x & ((1 << lg) - 1)) * 8;
+        if (unit < a.chunks && e < a.dim) sum_chunk<GDT, TDT, ACC>(a, unit, e);
+    }
+}
+
+// The runs that cross chunks: workgroup (c, tile) joins the run that begins
+// in chunk c and continues past it, 512 columns, the partial sums taken by
+// the four waves in turn and their sums added in the order of the waves.
+template <int TDT, bool ACC>
+__global__ __launch_bounds__(ROW_BLOCK) void embedding_join(SumArgs a) {
+    constexpr int WAVES = ROW_BLOCK / 64;
+    __shared__ float sums[WAVES][64 * 8];
+    const int64_t c = blockIdx.x;
+    const int64_t base = c * a.chunk, next = base + a.chunk;
+    if (next >= a.n) return;
+    const uint32_t key = a.keys[next];
+    if (key >= static_cast<uint32_t>(a.rows) || a.keys[next - 1] != key) return;
+    if (base > 0 && a.keys[base] == key && a.keys[base - 1] == key) return;  // began earlier
+    // chunks after c that the run reaches
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    int64_t reach = 0;
+    for (;;) {
+        const int64_t k = next + (reach + lane) * a.chunk;
+        const uint64_t on = __ballot(k < a.n && a.keys[k < a.n ? k : 0] == key);
+        if (on != ~uint64_t(0)) {
+            reach += __builtin_ctzll(~on);
+            break;
+        }
+        reach += 64;
+    }
+    const int64_t e = (int64_t(blockIdx.y) * 64 + lane) * 8;
+    f32x8 acc = 0.0f;
+    if (e < a.dim) {
+        for (int64_t i = wave; i <= reach; i += WAVES) {
+            const float *slot = a.partials + (i == 0 ? 2 * c + 1 : 2 * (c + i)) * a.dim;
+            if (e + 8 <= a.dim) {
+                const Raw8<G_F32> r = load_raw8<G_F32>(slot, e);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) acc[k] += raw_value<G_F32>(r, k);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (e + k < a.dim) acc[k] += slot[e + k];
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sums[wave][k * 64 + lane] = acc[k];
+    __syncthreads();
+    if (wave != 0 || e >= a.dim) return;
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[k] += sums[w][k * 64 + lane];
+    write_row<TDT, ACC>(a, key, e, acc);
+}
+
+// ------------------------------------------------------------- launchers --
+
+EmbeddingPlan embedding_plan(int64_t n, int64_t rows, int64_t dim) {
+    EmbeddingPlan p{};
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += (bytes + 255) / 256 * 256;
+        return here;
+    };
+    p.chunk = n < 4096 ? 8 : n < 32768 ? 16 : 32;
+    p.chunks = (n + p.chunk - 1) / p.chunk;
+    p.keys[0] = take(n * 4);
+    p.pos[0] = take(n * 4);
+    if (n > SORT_SMALL_MAX) {
+        p.keys[1] = take(n * 4);
+        p.pos[1] = take(n * 4);
+        p.counts = take((n + SORT_TILE - 1) / SORT_TILE * SORT_MAX_BINS * 4);
+    }
+    p.present = take((rows + 31) / 32 * 4);
+    p.partials = take(p.chunks * 2 * dim * 4);
+    p.bytes = at;
+    const int64_t pieces = (dim + 7) / 8;
+    const int lg = log2_ceil(pieces);
+    p.lg = lg < 3 ? 3 : lg > 6 ? 6 : lg;
+    p.tiles = static_cast<int32_t>((pieces + 63) / 64);
+    const int64_t units = p.lg == 6 ? p.chunks * p.tiles : p.chunks;
+    p.sum_blocks = (units + (int64_t(1) << (8 - p.lg)) - 1) >> (8 - p.lg);
+    // about 64-128 KiB per clearing workgroup, and at most 2^20 of them
+    p.rows_per_block = dim >= 32768 ? 1 : 32768 / dim;
+    if (p.rows_per_block < (rows >> 20)) p.rows_per_block = (rows >> 20) + 1;
+    p.clear_blocks = (rows + p.rows_per_block - 1) / p.rows_per_block;
+    return p;
+}
+
+template <int GDT, int TDT>
+static hipError_t launch_sums(const SumArgs &a, int lg, dim3 grid, hipStream_t stream, int *launched) {
+    const dim3 join(static_cast<unsigned>(a.chunks), static_cast<unsigned>((a.dim + 511) / 512)), block(ROW_BLOCK);
+    if (a.accumulate) hipLaunchKernelGGL((embedding_sum<GDT, TDT, true>), grid, block, 0, stream, a, lg);
+    else hipLaunchKernelGGL((embedding_sum<GDT, TDT, false>), grid, block, 0, stream, a, lg);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    ++*launched;
+    if (a.chunks < 2) return e;
+    if (a.accumulate) hipLaunchKernelGGL((embedding_join<TDT, true>), join, block, 0, stream, a);
+    else hipLaunchKernelGGL((embedding_join<TDT, false>), join, block, 0, stream, a);
+    e = hipGetLastError();
+    if (e == hipSuccess) ++*launched;
+    return e;
+}
+
+template <int GDT>
+static hipError_t launch_sums_to(const SumArgs &a, int tgdt, int lg, dim3 grid, hipStream_t stream, int *launched) {
+    switch (tgdt) {
+    case G_F32: return launch_sums<GDT, G_F32>(a, lg, grid, stream, launched);
+    case G_F16: return launch_sums<GDT, G_F16>(a, lg, grid, stream, launched);
+    default: return launch_sums<GDT, G_BF16>(a, lg, grid, stream, launched);
+    }
+}
+
+hipError_t launch_embedding_grad(const EmbeddingGradArgs &g, const EmbeddingPlan &p, int gdt, int tgdt,
+                                 hipStream_t stream, int *launched) {
+    auto words = [&](int64_t off) { return reinterpret_cast<uint32_t *>(g.workspace + off); };
+    uint32_t *present = g.accumulate ? nullptr : words(p.present);
+    SortKeys s{g.ids, nullptr, nullptr, g.n, g.rows, g.padding_id, g.wide_ids};
+    const int key_bits = log2_ceil(g.rows + 1);
+    hipError_t e;
+    int at = 0;  // the buffer that holds the sorted keys
+    if (g.n <= SORT_SMALL_MAX) {
+        const int passes = key_bits <= SORT_SMALL_BITS ? 1 : (key_bits + SORT_SMALL_BITS - 1) / SORT_SMALL_BITS;
+        const int bits = (key_bits + passes - 1) / passes;
+        hipLaunchKernelGGL(sort_small, dim3(1), dim3(SORT_SMALL_BLOCK), 0, stream, s, bits, passes, words(p.keys[0]),
+                           words(p.pos[0]), present);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        ++*launched;
+    } else {
+        const int passes = (key_bits + SORT_MAX_DIGIT_BITS - 1) / SORT_MAX_DIGIT_BITS;
+        const int bits = (key_bits + passes - 1) / passes;
+        const int64_t tiles = (g.n + SORT_TILE - 1) / SORT_TILE;
+        const dim3 grid(static_cast<unsigned>(tiles)), block(SORT_BLOCK);
+        uint32_t *counts = words(p.counts);
+        for (int pass = 0; pass < passes; ++pass) {
+            const int to = pass & 1;
+            const int shift = pass * bits;
+            if (pass == 0)
+                hipLaunchKernelGGL(radix_count<true>, grid, block, 0, stream, s, shift, bits, counts, present);
+            else hipLaunchKernelGGL(radix_count<false>, grid, block, 0, stream, s, shift, bits, counts, present);
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+            hipLaunchKernelGGL(radix_scan, dim3(1), dim3(SCAN_BLOCK), 0, stream, counts, tiles << bits);
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+            if (pass == 0)
+                hipLaunchKernelGGL(radix_scatter<true>, grid, block, 0, stream, s, shift, bits, counts,
+                                   words(p.keys[to]), words(p.pos[to]));
+            else
+                hipLaunchKernelGGL(radix_scatter<false>, grid, block, 0, stream, s, shift, bits, counts,
+                                   words(p.keys[to]), words(p.pos[to]));
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+            *launched += 3;
+            s.keys = words(p.keys[to]);
+            s.pos = words(p.pos[to]);
+            at = to;
+        }
+        if (present) {
+            hipLaunchKernelGGL(mark_present, dim3(static_cast<unsigned>((g.n + 255) / 256)), dim3(256), 0, stream,
+                               words(p.keys[at]), g.n, g.rows, present);
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+            ++*launched;
+        }
+    }
+    SumArgs a{};
+    a.grad_out = g.grad_out;
+    a.table_grad = g.table_grad;
+    a.keys = words(p.keys[at]);
+    a.pos = words(p.pos[at]);
+    a.present = present;
+    a.partials = reinterpret_cast<float *>(g.workspace + p.partials);
+    a.grad_stride = g.grad_stride;
+    a.table_stride = g.table_stride;
+    a.n = g.n;
+    a.rows = g.rows;
+    a.dim = g.dim;
+    a.chunk = p.chunk;
+    a.chunks = p.chunks;
+    a.accumulate = g.accumulate;
+    a.scale = g.scale;
+    a.tiles = p.tiles;
+    a.sum_blocks = p.sum_blocks;
+    a.rows_per_block = p.rows_per_block;
+    const int lg = p.lg;
+    const dim3 grid(static_cast<unsigned>(p.sum_blocks + (present ? p.clear_blocks : 0)));
+    switch (gdt) {
+    case G_F32: return launch_sums_to<G_F32>(a, tgdt, lg, grid, stream, launched);
+    case G_F16: return launch_sums_to<G_F16>(a, tgdt, lg, grid, stream, launched);
+    default: return launch_sums_to<G_BF16>(a, tgdt, lg, grid, stream, launched);
+    }
+}
+
+}  // namespace radamw

@@ -1,0 +1,595 @@
+// radamw_loss.hip -- the losses over a vocabulary's logits for gfx950: the
+// clipped policy loss with a KL term and the preference loss of sequence
+// pairs, with the gradient of the logits.
+//
+// For a row of logits x with label a:
+//   m = max x,  s = sum exp(x - m),  logp = (x_a - m) - log s
+//   d total / d x_j = coef * (1[j = a] - exp(x_j - m) / s)
+// where coef = d total / d logp is a number per row that each loss forms in
+// its own way.  Everything that is one number per row is formed in binary64
+// by one wave; the exponentials and their sums by lane are FP32.
+//
+// What bounds it is HBM: the logits are read once and their gradient written
+// once.  A workgroup holds a whole row in registers (up to 256 KiB: 1024
+// lanes x 16 chunks of 16 bytes), so that the maximum, the sum and the
+// gradient need one read; longer rows are read twice.
+#include "radamw_rows.h"
+#include "radamw_vocab.h"
+
+namespace radamw {
+
+namespace {
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, 64));
+    return v;
+}
+
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
+    return v;
+}
+
+// exp(y) for y <= 0 (v_exp_f32 is within 1 ulp; the product's rounding adds
+// |y| * 2^-24 relative, where exp(y) is correspondingly small).
+__device__ __forceinline__ float exp_neg(float y) { return __builtin_amdgcn_exp2f(y * LOG2E); }
+
+// -inf in every value of a chunk.
+template <int DT>
+__device__ __forceinline__ u32x4 lowest_chunk() {
+    const uint32_t w = DT == G_F32 ? 0xff800000u : DT == G_F16 ? 0xfc00fc00u : 0xff80ff80u;
+    return u32x4{w, w, w, w};
+}
+
+// The last, partial chunk of a row: `left` values at element e, -inf behind.
+template <int DT>
+__device__ __forceinline__ u32x4 load_partial(const void *p, int64_t e, int left) {
+    constexpr int E = chunk_elems<DT>;
+    u32x4 c = lowest_chunk<DT>();
+#pragma unroll
+    for (int j = 0; j < E - 1; ++j) {
+        if (j < left) {
+            const uint32_t b = load_bits<DT>(p, e + j);
+            if constexpr (DT == G_F32) c[j] = b;
+            else c[j >> 1] = j & 1 ? (c[j >> 1] & 0xffffu) | b << 16 : (c[j >> 1] & 0xffff0000u) | b;
+        }
+    }
+    return c;
+}
+
+template <int DT>
+__device__ __forceinline__ void store_partial(void *p, int64_t e, int left, const float *v) {
+#pragma unroll
+    for (int j = 0; j < chunk_elems<DT> - 1; ++j)
+        if (j < left) store_value<DT>(p, e + j, v[j]);
+}
+
+template <int DT>
+__device__ __forceinline__ void store_values(void *p, int64_t e, const float *v) {
+    if constexpr (DT == G_F32) {
+        const f32x4 x = {v[0], v[1], v[2], v[3]};
+        store_chunk<DT>(p, e, __builtin_bit_cast(u32x4, x));
+    } else {
+        f32x8 x;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = v[j];
+        store8<DT>(p, e, x);
+    }
+}
+
+// A row that takes no part: a gradient of zeros.
+template <int DT, int NT>
+__device__ __forceinline__ void zero_row(void *row, int64_t vocab) {
+    constexpr int E = chunk_elems<DT>;
+    const u32x4 z = {0, 0, 0, 0};
+    const int64_t full = vocab / E;
+    for (int64_t k = threadIdx.x; k < full; k += NT) store_chunk<DT>(row, k * E, z);
+    const int64_t e = full * E + threadIdx.x;
+    if (e < vocab) store_value<DT>(row, e, 0.0f);
+}
+
+// What a row's own scalars give: formed by one wave.
+struct RowResult {
+    double coef;       // d total / d logp
+    double one_less_p; // 1 - exp(logp)
+};
+
+// The clipped policy loss of one row.
+struct PolicyRow {
+    const float *old_logp, *ref_logp, *advantages, *weights;
+    float *loss;
+    double clip_low, clip_high, kl_coef;
+
+    // Lane 0 of the calling wave writes the row's loss.  The three
+    // exponentials of a row are evaluated at once, in lanes 0, 1 and 2.
+    __device__ __forceinline__ RowResult operator()(int64_t row, double logp) const {
+        const int lane = threadIdx.x & 63;
+        const double old = old_logp ? double(old_logp[row]) : logp;
+        const double ref = kl_coef != 0.0 ? double(ref_logp[row]) : logp;
+        const double arg = lane == 0 ? logp - old : lane == 1 ? ref - logp : logp;
+        const double em1 = expm1(arg);
+        const double r1 = __shfl(em1, 0, 64), k1 = __shfl(em1, 1, 64), p1 = __shfl(em1, 2, 64);
+        const double ratio = r1 + 1.0, adv = advantages[row], w = weights ? double(weights[row]) : 1.0;
+        const double lo = 1.0 - clip_low, hi = 1.0 + clip_high;
+        const double clipped = ratio < lo ? lo : ratio > hi ? hi : ratio;
+        const double plain = ratio * adv, held = clipped * adv;
+        // a NaN ratio or advantage stays NaN: neither comparison holds for it
+        double l = -(held < plain ? held : plain);
+        const bool active = adv >= 0.0 ? !(ratio > hi) : !(ratio < lo);
+        double d = active ? -plain : 0.0;
+        if (kl_coef != 0.0) {
+            l += kl_coef * (k1 - (ref - logp));
+            d -= kl_coef * k1;
+        }
+        if (lane == 0) loss[row] = static_cast<float>(l);
+        return {d * w, -p1};
+    }
+};
+
+// The preference loss's first pass keeps logp alone: what FP32 drops of it
+// goes into the record, so that sequence sums have all of it.
+struct LogpRow {};
+
+template <typename ROW>
+struct IsPolicy {
+    static constexpr bool value = false;
+};
+template <>
+struct IsPolicy<PolicyRow> {
+    static constexpr bool value = true;
+};
+
+template <typename ROW>
+__device__ __forceinline__ bool takes_part(const ROW &f, const LogitsArgs &x, int64_t row, int64_t *label) {
+    const int64_t a = load_index(x.labels, x.wide_ids, row);
+    *label = a;
+    bool in = a >= 0 && a < x.vocab;
+    if constexpr (IsPolicy<ROW>::value) {
+        if (in && f.weights) in = !(f.weights[row] == 0.0f);
+    }
+    return in;
+}
+
+template <typename ROW>
+__device__ __forceinline__ void absent_row(const ROW &f, const LogitsArgs &x, int64_t row) {
+    if (threadIdx.x == 0) {
+        x.logp[row] = 0.0f;
+        if constexpr (IsPolicy<ROW>::value) f.loss[row] = 0.0f;
+        if (x.stats) x.stats[row] = RowStats{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+}
+
+// The row's scalars from its maximum, sum and the label's logit, by every
+// wave that calls it (lane 0 of the wave with `write` stores).
+template <typename ROW>
+__device__ __forceinline__ RowResult finish_row(const ROW &f, const LogitsArgs &x, int64_t row, float top, double sum,
+                                                float at_label) {
+    const double logp = (double(at_label) - double(top)) - log(sum);
+    const float lp = static_cast<float>(logp);
+    if ((threadIdx.x & 63) == 0) x.logp[row] = lp;
+    RowResult r{0.0, 0.0};
+    if constexpr (IsPolicy<ROW>::value) {
+        r = f(row, logp);
+        if (x.stats && (threadIdx.x & 63) == 0)
+            x.stats[row] = RowStats{top, static_cast<float>(1.0 / sum), static_cast<float>(r.coef),
+                                    static_cast<float>(r.one_less_p)};
+    } else {
+        if ((threadIdx.x & 63) == 0)
+            x.stats[row] = RowStats{top, static_cast<float>(1.0 / sum), static_cast<float>(logp - double(lp)),
+                                    static_cast<float>(-expm1(logp))};
+    }
+    return r;
+}
+
+// ------------------------------------------------- rows held in registers --
+
+// One workgroup per row; lane tid holds chunks tid, tid + NT, ...
+template <int DT, int NT, int CH, bool GRAD, typename ROW>
+__global__ __launch_bounds__(NT) void loss_rows(LogitsArgs x, ROW f) {
+    constexpr int E = chunk_elems<DT>, WAVES = NT / 64;
+    __shared__ float tops[WAVES];
+    __shared__ double sums[WAVES];
+    __shared__ float label_coef[2];
+    const int64_t row = blockIdx.x;
+    const int tid = threadIdx.x, wave = tid >> 6;
+    char *out = static_cast<char *>(x.grad) + row * x.grad_stride * elem_bytes<DT>;
+    int64_t label;
+    if (!takes_part(f, x, row, &label)) {
+        absent_row(f, x, row);
+        if constexpr (GRAD) zero_row<DT, NT>(out, x.vocab);
+        return;
+    }
+    const char *in = static_cast<const char *>(x.logits) + row * x.stride * elem_bytes<DT>;
+    const int vocab = static_cast<int>(x.vocab), full = vocab / E, left = vocab % E;
+    const int used = (full + (left != 0) + NT - 1) / NT;  // chunks of the busiest lane
+    const float at_label = load_value<DT>(in, label);
+    u32x4 c[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int k = tid + i * NT;
+        if (k < full) c[i] = load_chunk<DT>(in, int64_t(k) * E);
+        else c[i] = lowest_chunk<DT>();
+    }
+    if (left && full < CH * NT && tid == full % NT) {
+        const u32x4 t = load_partial<DT>(in, int64_t(full) * E, left);
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+            if (i == full / NT) c[i] = t;
+    }
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        if (i < used) {
+#pragma unroll
+            for (int j = 0; j < E; ++j) top = fmaxf(top, chunk_value<DT>(c[i], j));
+        }
+    }
+    top = wave_max(top);
+    if ((tid & 63) == 0) tops[wave] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) top = fmaxf(top, tops[w]);
+    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        if (i < used) {
+#pragma unroll
+            for (int j = 0; j < E; ++j) part[j & 3] += exp_neg(chunk_value<DT>(c[i], j) - top);
+        }
+    }
+    double sum = wave_sum((double(part[0]) + double(part[1])) + (double(part[2]) + double(part[3])));
+    if ((tid & 63) == 0) sums[wave] = sum;
+    __syncthreads();
+    sum = 0.0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) sum += sums[w];
+    if (wave == 0) {
+        const RowResult r = finish_row(f, x, row, top, sum, at_label);
+        if (GRAD && tid == 0) {
+            const double g = r.coef * double(x.grad_scale);
+            label_coef[0] = static_cast<float>(-g / sum);
+            label_coef[1] = static_cast<float>(g * r.one_less_p);
+        }
+    }
+    if constexpr (GRAD) {
+        __syncthreads();
+        const float k = label_coef[0];
+        if (k == 0.0f && label_coef[1] == 0.0f) {  // a clipped row
+            zero_row<DT, NT>(out, x.vocab);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const int at = tid + i * NT;
+            if (i < used) {
+                float v[E];
+#pragma unroll
+                for (int j = 0; j < E; ++j) v[j] = exp_neg(chunk_value<DT>(c[i], j) - top) * k;
+                if (at < full) store_values<DT>(out, int64_t(at) * E, v);
+                else if (at == full && left) store_partial<DT>(out, int64_t(full) * E, left, v);
+            }
+        }
+        // the label's value, behind its own lane's store of the chunk
+        if (tid == static_cast<int>(label / E) % NT) store_value<DT>(out, label, label_coef[1]);
+    }
+}
+
+// --------------------------------------------------------- longer rows --
+
+constexpr int STREAM_BLOCK = 512;
+
+// Two reads of the row: the running maximum and sum by lane, then the
+// gradient.
+template <int DT, bool GRAD, typename ROW>
+__global__ __launch_bounds__(STREAM_BLOCK) void loss_rows_long(LogitsArgs x, ROW f) {
+    constexpr int E = chunk_elems<DT>, NT = STREAM_BLOCK, WAVES = NT / 64, U = 4;
+    __shared__ float tops[WAVES];
+    __shared__ double sums[WAVES];
+    __shared__ float label_coef[2];
+    const int64_t row = blockIdx.x;
+    const int tid = threadIdx.x, wave = tid >> 6;
+    char *out = static_cast<char *>(x.grad) + row * x.grad_stride * elem_bytes<DT>;
+    int64_t label;
+    if (!takes_part(f, x, row, &label)) {
+        absent_row(f, x, row);
+        if constexpr (GRAD) zero_row<DT, NT>(out, x.vocab);
+        return;
+    }
+    const char *in = static_cast<const char *>(x.logits) + row * x.stride * elem_bytes<DT>;
+    const int64_t full = x.vocab / E;
+    const int left = static_cast<int>(x.vocab % E);
+    const float at_label = load_value<DT>(in, label);
+    float top = -__builtin_inff();
+    double sum = 0.0;
+    const auto take = [&](const u32x4 (&c)[U]) {
+        float t = top;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < E; ++j) t = fmaxf(t, chunk_value<DT>(c[u], j));
+        // a lane that has seen only -inf sums zeros (and any NaN)
+        const float ref = t == -__builtin_inff() ? 0.0f : t;
+        float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < E; ++j) part[j & 3] += exp_neg(chunk_value<DT>(c[u], j) - ref);
+        sum = sum * double(exp_neg(top - ref)) + ((double(part[0]) + double(part[1])) + (double(part[2]) + double(part[3])));
+        top = t;
+    };
+    for (int64_t k0 = 0; k0 < full; k0 += NT * U) {
+        u32x4 c[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t k = k0 + u * NT + tid;
+            if (k < full) c[u] = load_chunk<DT>(in, k * E);
+            else c[u] = lowest_chunk<DT>();
+        }
+        take(c);
+    }
+    if (left && tid == 0) {
+        u32x4 c[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) c[u] = lowest_chunk<DT>();
+        c[0] = load_partial<DT>(in, full * E, left);
+        take(c);
+    }
+    float all = wave_max(top);
+    if ((tid & 63) == 0) tops[wave] = all;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) all = fmaxf(all, tops[w]);
+    sum = wave_sum(sum * double(exp_neg(top - all)));
+    if ((tid & 63) == 0) sums[wave] = sum;
+    __syncthreads();
+    sum = 0.0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) sum += sums[w];
+    if (wave == 0) {
+        const RowResult r = finish_row(f, x, row, all, sum, at_label);
+        if (GRAD && tid == 0) {
+            const double g = r.coef * double(x.grad_scale);
+            label_coef[0] = static_cast<float>(-g / sum);
+            label_coef[1] = static_cast<float>(g * r.one_less_p);
+        }
+    }
+    if constexpr (GRAD) {
+        __syncthreads();
+        const float k = label_coef[0];
+        if (k == 0.0f && label_coef[1] == 0.0f) {
+            zero_row<DT, NT>(out, x.vocab);
+            return;
+        }
+        for (int64_t k0 = 0; k0 < full; k0 += NT * U) {
+            u32x4 c[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t at = k0 + u * NT + tid;
+                if (at < full) c[u] = load_chunk<DT>(in, at * E);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t at = k0 + u * NT + tid;
+                if (at >= full) continue;
+                float v[E];
+#pragma unroll
+                for (int j = 0; j < E; ++j) v[j] = exp_neg(chunk_value<DT>(c[u], j) - all) * k;
+                store_values<DT>(out, at * E, v);
+            }
+        }
+        if (left && full % NT == tid) {
+            const u32x4 c = load_partial<DT>(in, full * E, left);
+            float v[E];
+#pragma unroll
+            for (int j = 0; j < E; ++j) v[j] = exp_neg(chunk_value<DT>(c, j) - all) * k;
+            store_partial<DT>(out, full * E, left, v);
+        }
+        if (tid == static_cast<int>((label / E) % NT)) store_value<DT>(out, label, label_coef[1]);
+    }
+}
+
+// ------------------------------------------- gradient from saved records --
+
+constexpr int GRAD_BLOCK = 256;
+constexpr int GRAD_UNROLL = 4;
+
+// Workgroup (row, part): GRAD_BLOCK * GRAD_UNROLL chunks of one row.
+template <int DT>
+__global__ __launch_bounds__(GRAD_BLOCK) void logits_grad(LogitsArgs x, const float *upstream) {
+    constexpr int E = chunk_elems<DT>;
+    const int64_t row = blockIdx.x;
+    const int64_t first = int64_t(blockIdx.y) * GRAD_BLOCK * GRAD_UNROLL;
+    char *out = static_cast<char *>(x.grad) + row * x.grad_stride * elem_bytes<DT>;
+    const char *in = static_cast<const char *>(x.logits) + row * x.stride * elem_bytes<DT>;
+    const int64_t full = x.vocab / E;
+    const int left = static_cast<int>(x.vocab % E);
+    const RowStats s = x.stats[row];
+    const float up = upstream ? *upstream : 1.0f;
+    const double g = double(s.coef) * double(x.grad_scale) * double(up);
+    const int64_t label = load_index(x.labels, x.wide_ids, row);
+    // no part in the loss (its record is all zeros), or clipped
+    const bool dead = s.coef == 0.0f || label < 0 || label >= x.vocab;
+    const float k = static_cast<float>(-g * double(s.inv_sum));
+    const float at_label = static_cast<float>(g * double(s.one_less_p));
+    u32x4 c[GRAD_UNROLL];
+#pragma unroll
+    for (int u = 0; u < GRAD_UNROLL; ++u) {
+        const int64_t at = first + u * GRAD_BLOCK + threadIdx.x;
+        if (!dead && at < full) c[u] = load_chunk<DT>(in, at * E);
+    }
+#pragma unroll
+    for (int u = 0; u < GRAD_UNROLL; ++u) {
+        const int64_t at = first + u * GRAD_BLOCK + threadIdx.x;
+        float v[E];
+        if (at < full) {
+#pragma unroll
+            for (int j = 0; j < E; ++j) v[j] = dead ? 0.0f : exp_neg(chunk_value<DT>(c[u], j) - s.max) * k;
+            store_values<DT>(out, at * E, v);
+        } else if (at == full && left) {
+            const u32x4 t = dead ? u32x4{0, 0, 0, 0} : load_partial<DT>(in, full * E, left);
+#pragma unroll
+            for (int j = 0; j < E; ++j) v[j] = dead ? 0.0f : exp_neg(chunk_value<DT>(t, j) - s.max) * k;
+            store_partial<DT>(out, full * E, left, v);
+        }
+        if (!dead && at == label / E) store_value<DT>(out, label, at_label);
+    }
+}
+
+// ----------------------------------------------------------- small sums --
+
+constexpr int TOTAL_BLOCK = 1024;
+
+// Sum over a workgroup, to every lane.
+template <int BLOCK>
+__device__ __forceinline__ double block_sum(double v, double *part) {
+    v = wave_sum(v);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0.0;
+#pragma unroll
+    for (int w = 0; w < BLOCK / 64; ++w) v += part[w];
+    __syncthreads();
+    return v;
+}
+
+// total = sum of weights[i] * loss[i] in a fixed order; entries of weight
+// zero add nothing, whatever their loss.
+__global__ __launch_bounds__(TOTAL_BLOCK) void weighted_total(const float *loss, const float *weights, int64_t n,
+                                                              float *total) {
+    __shared__ double part[TOTAL_BLOCK / 64];
+    double s = 0.0;
+    for (int64_t i = threadIdx.x; i < n; i += TOTAL_BLOCK) {
+        const float w = weights ? weights[i] : 1.0f;
+        if (w != 0.0f) s += double(w) * double(loss[i]);
+    }
+    s = block_sum<TOTAL_BLOCK>(s, part);
+    if (threadIdx.x == 0) *total = static_cast<float>(s);
+}
+
+constexpr int PAIR_BLOCK = 256;
+
+// Offset s, held to the rows there are.
+__device__ __forceinline__ int64_t row_offset(const PreferenceArgs &a, int64_t s) {
+    const int64_t o = load_index(a.offsets, a.x.wide_ids, s);
+    return o < 0 ? 0 : o > a.x.n ? a.x.n : o;
+}
+
+// One pair: the sums of its two sequences' log-probabilities, its loss, and
+// the rows' coefficients.
+__global__ __launch_bounds__(PAIR_BLOCK) void preference_pairs(PreferenceArgs a) {
+    __shared__ double part[PAIR_BLOCK / 64];
+    const int64_t pair = blockIdx.x;
+    int64_t begin[2], end[2];
+    double sum[2];
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+        const int64_t s = pair + side * a.pairs;
+        const int64_t b = row_offset(a, s), e = row_offset(a, s + 1);
+        begin[side] = b;
+        end[side] = e;
+        double v = 0.0;
+        for (int64_t i = b + threadIdx.x; i < e; i += PAIR_BLOCK)
+            v += double(a.x.logp[i]) + double(a.x.stats[i].coef);  // coef: what FP32 dropped of logp
+        sum[side] = block_sum<PAIR_BLOCK>(v, part);
+    }
+    const double h = a.beta * ((sum[0] - double(a.ref_logp[pair])) - (sum[1] - double(a.ref_logp[pair + a.pairs])));
+    // log sigmoid(h) = min(h, 0) - log1p(exp(-|h|))
+    const double q = exp(-fabs(h)), tail = log1p(q);
+    const double up = (h >= 0.0 ? 1.0 : q) / (1.0 + q), down = (h >= 0.0 ? q : 1.0) / (1.0 + q);  // sigmoid(h), sigmoid(-h)
+    const double ls = a.label_smoothing, w = a.weights ? double(a.weights[pair]) : 1.0;
+    if (threadIdx.x == 0) {
+        const double plus = h > 0.0 ? 0.0 : -h, minus = h < 0.0 ? 0.0 : h;
+        a.loss[pair] = static_cast<float>((1.0 - ls) * (plus + tail) + ls * (minus + tail));
+        a.seq_logp[pair] = static_cast<float>(sum[0]);
+        a.seq_logp[pair + a.pairs] = static_cast<float>(sum[1]);
+    }
+    const float coef = w == 0.0 ? 0.0f : static_cast<float>(w * a.beta * (ls * up - (1.0 - ls) * down));
+#pragma unroll
+    for (int side = 0; side < 2; ++side)
+        for (int64_t i = begin[side] + threadIdx.x; i < end[side]; i += PAIR_BLOCK)
+            if (a.x.stats[i].inv_sum != 0.0f) a.x.stats[i].coef = side ? -coef : coef;
+    if (pair != 0) return;
+    // rows outside every sequence have no coefficient
+    const int64_t first = row_offset(a, 0), last = row_offset(a, 2 * a.pairs);
+    for (int64_t i = threadIdx.x; i < first; i += PAIR_BLOCK) a.x.stats[i].coef = 0.0f;
+    for (int64_t i = last + threadIdx.x; i < a.x.n; i += PAIR_BLOCK) a.x.stats[i].coef = 0.0f;
+}
+
+}  // namespace
+
+// ------------------------------------------------------------- launchers --
+
+template <int DT, bool GRAD, typename ROW>
+static hipError_t launch_rows(const LogitsArgs &x, const ROW &f, hipStream_t stream) {
+    const int64_t chunks = (x.vocab + chunk_elems<DT> - 1) / chunk_elems<DT>;
+    const dim3 grid(static_cast<unsigned>(x.n));
+#define RADAMW_ROWS(NT, CH) \
+    hipLaunchKernelGGL((loss_rows<DT, NT, CH, GRAD, ROW>), grid, dim3(NT), 0, stream, x, f)
+    if (chunks <= 256 * 4) RADAMW_ROWS(256, 4);
+    else if (chunks <= 256 * 8) RADAMW_ROWS(256, 8);
+    else if (chunks <= 256 * 16) RADAMW_ROWS(256, 16);
+    else if (chunks <= 512 * 16) RADAMW_ROWS(512, 16);
+    else if (chunks <= 1024 * 16) RADAMW_ROWS(1024, 16);
+    else hipLaunchKernelGGL((loss_rows_long<DT, GRAD, ROW>), grid, dim3(STREAM_BLOCK), 0, stream, x, f);
+#undef RADAMW_ROWS
+    return hipGetLastError();
+}
+
+template <int DT>
+static hipError_t policy_rows(const LogitsArgs &x, const PolicyRow &f, hipStream_t stream) {
+    return x.grad ? launch_rows<DT, true>(x, f, stream) : launch_rows<DT, false>(x, f, stream);
+}
+
+hipError_t launch_policy_loss(const PolicyArgs &a, int dt, hipStream_t stream, int *launched) {
+    const PolicyRow f{a.old_logp, a.ref_logp, a.advantages, a.weights, a.loss, a.clip_low, a.clip_high, a.kl_coef};
+    hipError_t e = hipSuccess;
+    if (a.x.n > 0) {
+        e = dt == G_F32 ? policy_rows<G_F32>(a.x, f, stream)
+            : dt == G_F16 ? policy_rows<G_F16>(a.x, f, stream) : policy_rows<G_BF16>(a.x, f, stream);
+        if (e != hipSuccess) return e;
+        ++*launched;
+    }
+    hipLaunchKernelGGL(weighted_total, dim3(1), dim3(TOTAL_BLOCK), 0, stream, a.loss, a.weights, a.x.n, a.total);
+    if ((e = hipGetLastError()) == hipSuccess) ++*launched;
+    return e;
+}
+
+hipError_t launch_logits_grad(const LogitsArgs &x, const float *upstream, int dt, hipStream_t stream) {
+    const int64_t chunks = (x.vocab + (dt == G_F32 ? 3 : 7)) / (dt == G_F32 ? 4 : 8);
+    const int64_t per = int64_t(GRAD_BLOCK) * GRAD_UNROLL;
+    const dim3 grid(static_cast<unsigned>(x.n), static_cast<unsigned>((chunks + per - 1) / per)), block(GRAD_BLOCK);
+    switch (dt) {
+    case G_F32: hipLaunchKernelGGL(logits_grad<G_F32>, grid, block, 0, stream, x, upstream); break;
+    case G_F16: hipLaunchKernelGGL(logits_grad<G_F16>, grid, block, 0, stream, x, upstream); break;
+    default: hipLaunchKernelGGL(logits_grad<G_BF16>, grid, block, 0, stream, x, upstream); break;
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_preference_loss(const PreferenceArgs &a, int dt, hipStream_t stream, int *launched) {
+    const LogpRow f{};
+    hipError_t e = hipSuccess;
+    if (a.x.n > 0) {
+        e = dt == G_F32 ? launch_rows<G_F32, false>(a.x, f, stream)
+            : dt == G_F16 ? launch_rows<G_F16, false>(a.x, f, stream) : launch_rows<G_BF16, false>(a.x, f, stream);
+        if (e != hipSuccess) return e;
+        ++*launched;
+    }
+    if (a.pairs > 0) {
+        hipLaunchKernelGGL(preference_pairs, dim3(static_cast<unsigned>(a.pairs)), dim3(PAIR_BLOCK), 0, stream, a);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        ++*launched;
+    }
+    hipLaunchKernelGGL(weighted_total, dim3(1), dim3(TOTAL_BLOCK), 0, stream, a.loss, a.weights, a.pairs, a.total);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    ++*launched;
+    if (a.x.grad && a.x.n > 0) {
+        if ((e = launch_logits_grad(a.x, nullptr, dt, stream)) != hipSuccess) return e;
+        ++*launched;
+    }
+    return e;
+}
+
+}  // namespace radamw
