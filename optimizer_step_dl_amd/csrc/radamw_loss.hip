@@ -9,12 +9,23 @@
 // its own way.  Everything that is one number per row is formed in binary64
 // by one wave; the exponentials and their sums by lane are FP32.
 //
+// An exponential is exp2(x * L - c), one FMA and one v_exp_f32, with
+// c = fl(m * L) and L = log2 e: the rounding of c shifts every exponent of
+// the row alike and cancels in p_j = e_j / s and, in binary64, in logp.
+// That holds while |m| < 2^24 (c is then off by at most 1); other rows, and
+// those whose maximum is infinite or NaN, take slow_row, which forms x - m
+// first and reads the row again.
+//
 // What bounds it is HBM: the logits are read once and their gradient written
 // once.  A workgroup holds a whole row in registers (up to 256 KiB: 1024
 // lanes x 16 chunks of 16 bytes), so that the maximum, the sum and the
 // gradient need one read; longer rows are read twice.
 #include "radamw_rows.h"
 #include "radamw_vocab.h"
+
+// c = fl(m * LOG2E) has to be the same number wherever it is used: a product
+// fused into one of its uses would not be.
+#pragma clang fp contract(off)
 
 namespace radamw {
 
@@ -32,8 +43,30 @@ __device__ __forceinline__ double wave_sum(double v) {
     return v;
 }
 
-// exp(y) for y <= 0 (v_exp_f32 is within 1 ulp; the product's rounding adds
-// |y| * 2^-24 relative, where exp(y) is correspondingly small).
+constexpr double LN2 = 0.6931471805599453;
+constexpr float LOG2E_LOW = static_cast<float>(1.4426950408889634 - double(LOG2E));
+
+// logp of a label's logit, in the same scale as the exponentials.
+template <bool EXACT>
+__device__ __forceinline__ double label_logp(float at_label, float shift, double sum) {
+    const double scale = EXACT ? 1.4426950408889634 : double(LOG2E);
+    return (double(at_label) * scale - double(shift)) * LN2 - log(sum);
+}
+
+// Rows whose exponents are shifted by c = fl(max * LOG2E).
+__device__ __forceinline__ bool shiftable(float top) { return fabsf(top) < 16777216.0f; }
+
+// exp2(x * LOG2E - c).  LOG2E alone is off by 1.3e-8, which changes p_j by
+// that much of x and logp by 1.3e-8 (x_a - mean x); EXACT adds the rest of
+// the constant, for sequence sums, where a bias of every token adds up.
+template <bool EXACT>
+__device__ __forceinline__ float exp_shifted(float x, float c) {
+    float t = __builtin_fmaf(x, LOG2E, -c);
+    if constexpr (EXACT) t = __builtin_fmaf(x, LOG2E_LOW, t);
+    return __builtin_amdgcn_exp2f(t);
+}
+
+// exp(y) for y <= 0, the slow rows' form.
 __device__ __forceinline__ float exp_neg(float y) { return __builtin_amdgcn_exp2f(y * LOG2E); }
 
 // -inf in every value of a chunk.
@@ -70,12 +103,11 @@ template <int DT>
 __device__ __forceinline__ void store_values(void *p, int64_t e, const float *v) {
     if constexpr (DT == G_F32) {
         const f32x4 x = {v[0], v[1], v[2], v[3]};
-        store_chunk<DT>(p, e, __builtin_bit_cast(u32x4, x));
+        stream_out<DT>(p, e, __builtin_bit_cast(u32x4, x));
     } else {
-        f32x8 x;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = v[j];
-        store8<DT>(p, e, x);
+        const f32x8 x = {v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]};
+        if constexpr (DT == G_F16) stream_out<DT>(p, e, __builtin_bit_cast(u32x4, __builtin_convertvector(x, f16x8)));
+        else stream_out<DT>(p, e, __builtin_bit_cast(u32x4, __builtin_convertvector(x, bf16x8)));
     }
 }
 
@@ -85,7 +117,7 @@ __device__ __forceinline__ void zero_row(void *row, int64_t vocab) {
     constexpr int E = chunk_elems<DT>;
     const u32x4 z = {0, 0, 0, 0};
     const int64_t full = vocab / E;
-    for (int64_t k = threadIdx.x; k < full; k += NT) store_chunk<DT>(row, k * E, z);
+    for (int64_t k = threadIdx.x; k < full; k += NT) stream_out<DT>(row, k * E, z);
     const int64_t e = full * E + threadIdx.x;
     if (e < vocab) store_value<DT>(row, e, 0.0f);
 }
@@ -161,26 +193,80 @@ __device__ __forceinline__ void absent_row(const ROW &f, const LogitsArgs &x, in
     }
 }
 
-// The row's scalars from its maximum, sum and the label's logit, by every
-// wave that calls it (lane 0 of the wave with `write` stores).
+// The row's scalars from its maximum, log-probability and sum, by a whole
+// wave, whose lane 0 stores them.
 template <typename ROW>
 __device__ __forceinline__ RowResult finish_row(const ROW &f, const LogitsArgs &x, int64_t row, float top, double sum,
-                                                float at_label) {
-    const double logp = (double(at_label) - double(top)) - log(sum);
+                                                double logp) {
     const float lp = static_cast<float>(logp);
-    if ((threadIdx.x & 63) == 0) x.logp[row] = lp;
+    const bool lead = (threadIdx.x & 63) == 0;
+    if (lead) x.logp[row] = lp;
     RowResult r{0.0, 0.0};
     if constexpr (IsPolicy<ROW>::value) {
         r = f(row, logp);
-        if (x.stats && (threadIdx.x & 63) == 0)
+        if (x.stats && lead)
             x.stats[row] = RowStats{top, static_cast<float>(1.0 / sum), static_cast<float>(r.coef),
                                     static_cast<float>(r.one_less_p)};
     } else {
-        if ((threadIdx.x & 63) == 0)
-            x.stats[row] = RowStats{top, static_cast<float>(1.0 / sum), static_cast<float>(logp - double(lp)),
-                                    static_cast<float>(-expm1(logp))};
+        const float less = static_cast<float>(-expm1(logp));
+        if (lead) x.stats[row] = RowStats{top, static_cast<float>(1.0 / sum), static_cast<float>(logp - double(lp)), less};
     }
     return r;
+}
+
+// Sum over a workgroup, to every lane, in a fixed order.
+template <int NT>
+__device__ __forceinline__ double block_sum(double v, double *part) {
+    v = wave_sum(v);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0.0;
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) v += part[w];
+    return v;
+}
+
+// A workgroup's shared words for one row.
+template <int NT>
+struct RowShared {
+    float tops[NT / 64];
+    double sums[NT / 64];
+    float factor;    // of exp(x - m), for the gradient
+    float at_label;  // the label's gradient
+};
+
+// The factors of the gradient from a row's scalars (one lane).
+template <int NT>
+__device__ __forceinline__ void put_factors(RowShared<NT> &sh, const RowResult &r, double scale, double sum) {
+    const double g = r.coef * scale;
+    sh.factor = static_cast<float>(-g / sum);
+    sh.at_label = static_cast<float>(g * r.one_less_p);
+}
+
+// A row whose maximum is too large (or not a number) for shifted exponents:
+// two more reads, one chunk at a time.
+template <int DT, int NT, bool GRAD, typename ROW>
+__device__ __forceinline__ void slow_row(const LogitsArgs &x, const ROW &f, int64_t row, int64_t label, float top,
+                                      RowShared<NT> &sh) {
+    const char *in = static_cast<const char *>(x.logits) + row * x.stride * elem_bytes<DT>;
+    const float at_label = load_value<DT>(in, label);
+    double sum = 0.0;
+#pragma clang loop unroll(disable)
+    for (int64_t k = threadIdx.x; k < x.vocab; k += NT) sum += double(exp_neg(load_value<DT>(in, k) - top));
+    sum = block_sum<NT>(sum, sh.sums);
+    if (threadIdx.x < 64) {
+        const RowResult r = finish_row(f, x, row, top, sum, (double(at_label) - double(top)) - log(sum));
+        if (GRAD && threadIdx.x == 0) put_factors(sh, r, x.grad_scale, sum);
+    }
+    if constexpr (GRAD) {
+        char *out = static_cast<char *>(x.grad) + row * x.grad_stride * elem_bytes<DT>;
+        __syncthreads();
+#pragma clang loop unroll(disable)
+        for (int64_t k = threadIdx.x; k < x.vocab; k += NT) {
+            const float v = exp_neg(load_value<DT>(in, k) - top) * sh.factor;
+            store_value<DT>(out, k, k == label ? sh.at_label : v);
+        }
+    }
 }
 
 // ------------------------------------------------- rows held in registers --
@@ -189,9 +275,7 @@ __device__ __forceinline__ RowResult finish_row(const ROW &f, const LogitsArgs &
 template <int DT, int NT, int CH, bool GRAD, typename ROW>
 __global__ __launch_bounds__(NT) void loss_rows(LogitsArgs x, ROW f) {
     constexpr int E = chunk_elems<DT>, WAVES = NT / 64;
-    __shared__ float tops[WAVES];
-    __shared__ double sums[WAVES];
-    __shared__ float label_coef[2];
+    __shared__ RowShared<NT> sh;
     const int64_t row = blockIdx.x;
     const int tid = threadIdx.x, wave = tid >> 6;
     char *out = static_cast<char *>(x.grad) + row * x.grad_stride * elem_bytes<DT>;
@@ -209,10 +293,10 @@ __global__ __launch_bounds__(NT) void loss_rows(LogitsArgs x, ROW f) {
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
         const int k = tid + i * NT;
-        if (k < full) c[i] = load_chunk<DT>(in, int64_t(k) * E);
+        if (k < full) c[i] = stream_chunk<DT>(in, int64_t(k) * E);
         else c[i] = lowest_chunk<DT>();
     }
-    if (left && full < CH * NT && tid == full % NT) {
+    if (left && tid == full % NT) {
         const u32x4 t = load_partial<DT>(in, int64_t(full) * E, left);
 #pragma unroll
         for (int i = 0; i < CH; ++i)
@@ -227,36 +311,33 @@ __global__ __launch_bounds__(NT) void loss_rows(LogitsArgs x, ROW f) {
         }
     }
     top = wave_max(top);
-    if ((tid & 63) == 0) tops[wave] = top;
+    if ((tid & 63) == 0) sh.tops[wave] = top;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) top = fmaxf(top, tops[w]);
+    for (int w = 0; w < WAVES; ++w) top = fmaxf(top, sh.tops[w]);
+    if (!shiftable(top)) {
+        slow_row<DT, NT, GRAD>(x, f, row, label, top, sh);
+        return;
+    }
+    const float shift = top * LOG2E;
     float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
         if (i < used) {
 #pragma unroll
-            for (int j = 0; j < E; ++j) part[j & 3] += exp_neg(chunk_value<DT>(c[i], j) - top);
+            for (int j = 0; j < E; ++j) part[j & 3] += exp_shifted<!GRAD>(chunk_value<DT>(c[i], j), shift);
         }
     }
-    double sum = wave_sum((double(part[0]) + double(part[1])) + (double(part[2]) + double(part[3])));
-    if ((tid & 63) == 0) sums[wave] = sum;
-    __syncthreads();
-    sum = 0.0;
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w) sum += sums[w];
+    const double sum = block_sum<NT>((double(part[0]) + double(part[1])) + (double(part[2]) + double(part[3])), sh.sums);
     if (wave == 0) {
-        const RowResult r = finish_row(f, x, row, top, sum, at_label);
-        if (GRAD && tid == 0) {
-            const double g = r.coef * double(x.grad_scale);
-            label_coef[0] = static_cast<float>(-g / sum);
-            label_coef[1] = static_cast<float>(g * r.one_less_p);
-        }
+        const double logp = label_logp<!GRAD>(at_label, shift, sum);
+        const RowResult r = finish_row(f, x, row, top, sum, logp);
+        if (GRAD && tid == 0) put_factors(sh, r, x.grad_scale, sum);
     }
     if constexpr (GRAD) {
         __syncthreads();
-        const float k = label_coef[0];
-        if (k == 0.0f && label_coef[1] == 0.0f) {  // a clipped row
+        const float k = sh.factor;
+        if (k == 0.0f && sh.at_label == 0.0f) {  // a clipped row
             zero_row<DT, NT>(out, x.vocab);
             return;
         }
@@ -266,28 +347,39 @@ __global__ __launch_bounds__(NT) void loss_rows(LogitsArgs x, ROW f) {
             if (i < used) {
                 float v[E];
 #pragma unroll
-                for (int j = 0; j < E; ++j) v[j] = exp_neg(chunk_value<DT>(c[i], j) - top) * k;
+                for (int j = 0; j < E; ++j) v[j] = exp_shifted<false>(chunk_value<DT>(c[i], j), shift) * k;
                 if (at < full) store_values<DT>(out, int64_t(at) * E, v);
                 else if (at == full && left) store_partial<DT>(out, int64_t(full) * E, left, v);
             }
         }
         // the label's value, behind its own lane's store of the chunk
-        if (tid == static_cast<int>(label / E) % NT) store_value<DT>(out, label, label_coef[1]);
+        if (tid == static_cast<int>(label / E) % NT) store_value<DT>(out, label, sh.at_label);
     }
 }
 
-// --------------------------------------------------------- longer rows --
+// ----------------------------------------------------------- longer rows --
 
-constexpr int STREAM_BLOCK = 512;
+// A sum relative to exponent `from`, relative to `to`.  A lane without a
+// value yet has the sum 0 and no exponent; a NaN stays one.
+__device__ __forceinline__ double rescaled(double sum, float from, float to) {
+    return sum == 0.0 ? 0.0 : sum * double(__builtin_amdgcn_exp2f(from - to));
+}
 
-// Two reads of the row: the running maximum and sum by lane, then the
-// gradient.
+#ifndef RADAMW_STREAM_BLOCK
+#define RADAMW_STREAM_BLOCK 1024
+#endif
+constexpr int STREAM_BLOCK = RADAMW_STREAM_BLOCK;
+#ifndef RADAMW_STREAM_UNROLL
+#define RADAMW_STREAM_UNROLL 4
+#endif
+constexpr int STREAM_UNROLL = RADAMW_STREAM_UNROLL;  // chunks in flight per lane
+
+// The running maximum and sum by lane in one read; with the gradient, a
+// second one.
 template <int DT, bool GRAD, typename ROW>
 __global__ __launch_bounds__(STREAM_BLOCK) void loss_rows_long(LogitsArgs x, ROW f) {
-    constexpr int E = chunk_elems<DT>, NT = STREAM_BLOCK, WAVES = NT / 64, U = 4;
-    __shared__ float tops[WAVES];
-    __shared__ double sums[WAVES];
-    __shared__ float label_coef[2];
+    constexpr int E = chunk_elems<DT>, NT = STREAM_BLOCK, WAVES = NT / 64, U = STREAM_UNROLL;
+    __shared__ RowShared<NT> sh;
     const int64_t row = blockIdx.x;
     const int tid = threadIdx.x, wave = tid >> 6;
     char *out = static_cast<char *>(x.grad) + row * x.grad_stride * elem_bytes<DT>;
@@ -301,7 +393,10 @@ __global__ __launch_bounds__(STREAM_BLOCK) void loss_rows_long(LogitsArgs x, ROW
     const int64_t full = x.vocab / E;
     const int left = static_cast<int>(x.vocab % E);
     const float at_label = load_value<DT>(in, label);
-    float top = -__builtin_inff();
+    // top: the lane's largest value so far; shift: what its sum is relative
+    // to.  A lane that holds something else than a number, or a value too
+    // large to shift by, makes `top` of the row such a one, and the row slow.
+    float top = -__builtin_inff(), shift = 0.0f;
     double sum = 0.0;
     const auto take = [&](const u32x4 (&c)[U]) {
         float t = top;
@@ -309,22 +404,22 @@ __global__ __launch_bounds__(STREAM_BLOCK) void loss_rows_long(LogitsArgs x, ROW
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int j = 0; j < E; ++j) t = fmaxf(t, chunk_value<DT>(c[u], j));
-        // a lane that has seen only -inf sums zeros (and any NaN)
-        const float ref = t == -__builtin_inff() ? 0.0f : t;
+        const float to = shiftable(t) ? t * LOG2E : 0.0f;
         float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int j = 0; j < E; ++j) part[j & 3] += exp_neg(chunk_value<DT>(c[u], j) - ref);
-        sum = sum * double(exp_neg(top - ref)) + ((double(part[0]) + double(part[1])) + (double(part[2]) + double(part[3])));
+            for (int j = 0; j < E; ++j) part[j & 3] += exp_shifted<!GRAD>(chunk_value<DT>(c[u], j), to);
+        sum = rescaled(sum, shift, to) + ((double(part[0]) + double(part[1])) + (double(part[2]) + double(part[3])));
         top = t;
+        shift = to;
     };
     for (int64_t k0 = 0; k0 < full; k0 += NT * U) {
         u32x4 c[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t k = k0 + u * NT + tid;
-            if (k < full) c[u] = load_chunk<DT>(in, k * E);
+            if (k < full) c[u] = GRAD ? load_chunk<DT>(in, k * E) : stream_chunk<DT>(in, k * E);
             else c[u] = lowest_chunk<DT>();
         }
         take(c);
@@ -337,28 +432,26 @@ __global__ __launch_bounds__(STREAM_BLOCK) void loss_rows_long(LogitsArgs x, ROW
         take(c);
     }
     float all = wave_max(top);
-    if ((tid & 63) == 0) tops[wave] = all;
+    if ((tid & 63) == 0) sh.tops[wave] = all;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) all = fmaxf(all, tops[w]);
-    sum = wave_sum(sum * double(exp_neg(top - all)));
-    if ((tid & 63) == 0) sums[wave] = sum;
-    __syncthreads();
-    sum = 0.0;
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w) sum += sums[w];
+    for (int w = 0; w < WAVES; ++w) all = fmaxf(all, sh.tops[w]);
+    if (!shiftable(all)) {
+        slow_row<DT, NT, GRAD>(x, f, row, label, all, sh);
+        return;
+    }
+    const float to = all * LOG2E;
+    sum = block_sum<NT>(rescaled(sum, shift, to), sh.sums);
+    shift = to;
     if (wave == 0) {
-        const RowResult r = finish_row(f, x, row, all, sum, at_label);
-        if (GRAD && tid == 0) {
-            const double g = r.coef * double(x.grad_scale);
-            label_coef[0] = static_cast<float>(-g / sum);
-            label_coef[1] = static_cast<float>(g * r.one_less_p);
-        }
+        const double logp = label_logp<!GRAD>(at_label, shift, sum);
+        const RowResult r = finish_row(f, x, row, all, sum, logp);
+        if (GRAD && tid == 0) put_factors(sh, r, x.grad_scale, sum);
     }
     if constexpr (GRAD) {
         __syncthreads();
-        const float k = label_coef[0];
-        if (k == 0.0f && label_coef[1] == 0.0f) {
+        const float k = sh.factor;
+        if (k == 0.0f && sh.at_label == 0.0f) {
             zero_row<DT, NT>(out, x.vocab);
             return;
         }
@@ -367,7 +460,7 @@ __global__ __launch_bounds__(STREAM_BLOCK) void loss_rows_long(LogitsArgs x, ROW
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int64_t at = k0 + u * NT + tid;
-                if (at < full) c[u] = load_chunk<DT>(in, at * E);
+                if (at < full) c[u] = stream_chunk<DT>(in, at * E);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -375,7 +468,7 @@ __global__ __launch_bounds__(STREAM_BLOCK) void loss_rows_long(LogitsArgs x, ROW
                 if (at >= full) continue;
                 float v[E];
 #pragma unroll
-                for (int j = 0; j < E; ++j) v[j] = exp_neg(chunk_value<DT>(c[u], j) - all) * k;
+                for (int j = 0; j < E; ++j) v[j] = exp_shifted<false>(chunk_value<DT>(c[u], j), shift) * k;
                 store_values<DT>(out, at * E, v);
             }
         }
@@ -383,17 +476,23 @@ __global__ __launch_bounds__(STREAM_BLOCK) void loss_rows_long(LogitsArgs x, ROW
             const u32x4 c = load_partial<DT>(in, full * E, left);
             float v[E];
 #pragma unroll
-            for (int j = 0; j < E; ++j) v[j] = exp_neg(chunk_value<DT>(c, j) - all) * k;
+            for (int j = 0; j < E; ++j) v[j] = exp_shifted<false>(chunk_value<DT>(c, j), shift) * k;
             store_partial<DT>(out, full * E, left, v);
         }
-        if (tid == static_cast<int>((label / E) % NT)) store_value<DT>(out, label, label_coef[1]);
+        if (tid == static_cast<int>((label / E) % NT)) store_value<DT>(out, label, sh.at_label);
     }
 }
 
 // ------------------------------------------- gradient from saved records --
 
-constexpr int GRAD_BLOCK = 256;
-constexpr int GRAD_UNROLL = 4;
+#ifndef RADAMW_GRAD_BLOCK
+#define RADAMW_GRAD_BLOCK 256
+#endif
+#ifndef RADAMW_GRAD_UNROLL
+#define RADAMW_GRAD_UNROLL 4
+#endif
+constexpr int GRAD_BLOCK = RADAMW_GRAD_BLOCK;
+constexpr int GRAD_UNROLL = RADAMW_GRAD_UNROLL;
 
 // Workgroup (row, part): GRAD_BLOCK * GRAD_UNROLL chunks of one row.
 template <int DT>
@@ -413,11 +512,15 @@ __global__ __launch_bounds__(GRAD_BLOCK) void logits_grad(LogitsArgs x, const fl
     const bool dead = s.coef == 0.0f || label < 0 || label >= x.vocab;
     const float k = static_cast<float>(-g * double(s.inv_sum));
     const float at_label = static_cast<float>(g * double(s.one_less_p));
+    // shifted exponents, or x - m first, as the forward pass summed them
+    const bool fast = shiftable(s.max);
+    const float shift = s.max * LOG2E;
+    const auto value = [&](float z) { return (fast ? exp_shifted<false>(z, shift) : exp_neg(z - s.max)) * k; };
     u32x4 c[GRAD_UNROLL];
 #pragma unroll
     for (int u = 0; u < GRAD_UNROLL; ++u) {
         const int64_t at = first + u * GRAD_BLOCK + threadIdx.x;
-        if (!dead && at < full) c[u] = load_chunk<DT>(in, at * E);
+        if (!dead && at < full) c[u] = stream_chunk<DT>(in, at * E);
     }
 #pragma unroll
     for (int u = 0; u < GRAD_UNROLL; ++u) {
@@ -425,12 +528,12 @@ __global__ __launch_bounds__(GRAD_BLOCK) void logits_grad(LogitsArgs x, const fl
         float v[E];
         if (at < full) {
 #pragma unroll
-            for (int j = 0; j < E; ++j) v[j] = dead ? 0.0f : exp_neg(chunk_value<DT>(c[u], j) - s.max) * k;
+            for (int j = 0; j < E; ++j) v[j] = dead ? 0.0f : value(chunk_value<DT>(c[u], j));
             store_values<DT>(out, at * E, v);
         } else if (at == full && left) {
             const u32x4 t = dead ? u32x4{0, 0, 0, 0} : load_partial<DT>(in, full * E, left);
 #pragma unroll
-            for (int j = 0; j < E; ++j) v[j] = dead ? 0.0f : exp_neg(chunk_value<DT>(t, j) - s.max) * k;
+            for (int j = 0; j < E; ++j) v[j] = dead ? 0.0f : value(chunk_value<DT>(t, j));
             store_partial<DT>(out, full * E, left, v);
         }
         if (!dead && at == label / E) store_value<DT>(out, label, at_label);
@@ -440,19 +543,6 @@ __global__ __launch_bounds__(GRAD_BLOCK) void logits_grad(LogitsArgs x, const fl
 // ----------------------------------------------------------- small sums --
 
 constexpr int TOTAL_BLOCK = 1024;
-
-// Sum over a workgroup, to every lane.
-template <int BLOCK>
-__device__ __forceinline__ double block_sum(double v, double *part) {
-    v = wave_sum(v);
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = 0.0;
-#pragma unroll
-    for (int w = 0; w < BLOCK / 64; ++w) v += part[w];
-    __syncthreads();
-    return v;
-}
 
 // total = sum of weights[i] * loss[i] in a fixed order; entries of weight
 // zero add nothing, whatever their loss.
@@ -479,7 +569,7 @@ __device__ __forceinline__ int64_t row_offset(const PreferenceArgs &a, int64_t s
 // One pair: the sums of its two sequences' log-probabilities, its loss, and
 // the rows' coefficients.
 __global__ __launch_bounds__(PAIR_BLOCK) void preference_pairs(PreferenceArgs a) {
-    __shared__ double part[PAIR_BLOCK / 64];
+    __shared__ double part[2][PAIR_BLOCK / 64];
     const int64_t pair = blockIdx.x;
     int64_t begin[2], end[2];
     double sum[2];
@@ -492,7 +582,7 @@ __global__ __launch_bounds__(PAIR_BLOCK) void preference_pairs(PreferenceArgs a)
         double v = 0.0;
         for (int64_t i = b + threadIdx.x; i < e; i += PAIR_BLOCK)
             v += double(a.x.logp[i]) + double(a.x.stats[i].coef);  // coef: what FP32 dropped of logp
-        sum[side] = block_sum<PAIR_BLOCK>(v, part);
+        sum[side] = block_sum<PAIR_BLOCK>(v, part[side]);
     }
     const double h = a.beta * ((sum[0] - double(a.ref_logp[pair])) - (sum[1] - double(a.ref_logp[pair + a.pairs])));
     // log sigmoid(h) = min(h, 0) - log1p(exp(-|h|))
@@ -527,7 +617,9 @@ static hipError_t launch_rows(const LogitsArgs &x, const ROW &f, hipStream_t str
     const dim3 grid(static_cast<unsigned>(x.n));
 #define RADAMW_ROWS(NT, CH) \
     hipLaunchKernelGGL((loss_rows<DT, NT, CH, GRAD, ROW>), grid, dim3(NT), 0, stream, x, f)
-    if (chunks <= 256 * 4) RADAMW_ROWS(256, 4);
+    if (!GRAD && chunks > 256 * 4)
+        hipLaunchKernelGGL((loss_rows_long<DT, GRAD, ROW>), grid, dim3(STREAM_BLOCK), 0, stream, x, f);
+    else if (chunks <= 256 * 4) RADAMW_ROWS(256, 4);
     else if (chunks <= 256 * 8) RADAMW_ROWS(256, 8);
     else if (chunks <= 256 * 16) RADAMW_ROWS(256, 16);
     else if (chunks <= 512 * 16) RADAMW_ROWS(512, 16);

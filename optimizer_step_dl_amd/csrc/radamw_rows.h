@@ -33,6 +33,19 @@ __device__ __forceinline__ u32x4 load_chunk(const void *p, int64_t e) {
     if constexpr (DT == G_F32) return *(const RADAMW_GLOBAL u32x4_any4 *)(static_cast<const float *>(p) + e);
     else return *(const RADAMW_GLOBAL u32x4_any2 *)(static_cast<const uint16_t *>(p) + e);
 }
+// The same, with the nontemporal hint, for data that is touched once.
+template <int DT>
+__device__ __forceinline__ u32x4 stream_chunk(const void *p, int64_t e) {
+    if constexpr (DT == G_F32)
+        return __builtin_nontemporal_load((const RADAMW_GLOBAL u32x4_any4 *)(static_cast<const float *>(p) + e));
+    else return __builtin_nontemporal_load((const RADAMW_GLOBAL u32x4_any2 *)(static_cast<const uint16_t *>(p) + e));
+}
+template <int DT>
+__device__ __forceinline__ void stream_out(void *p, int64_t e, u32x4 v) {
+    if constexpr (DT == G_F32)
+        __builtin_nontemporal_store(v, (RADAMW_GLOBAL u32x4_any4 *)(static_cast<float *>(p) + e));
+    else __builtin_nontemporal_store(v, (RADAMW_GLOBAL u32x4_any2 *)(static_cast<uint16_t *>(p) + e));
+}
 template <int DT>
 __device__ __forceinline__ void store_chunk(void *p, int64_t e, u32x4 v) {
     if constexpr (DT == G_F32) *(RADAMW_GLOBAL u32x4_any4 *)(static_cast<float *>(p) + e) = v;

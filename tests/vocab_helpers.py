@@ -117,10 +117,9 @@ class Rows:
         p_err = self.p * (self.e_rel + self.err[:, None]) + 2.0 ** -126
         # the label's factor 1 - p comes from logp itself
         slack = 1.01 * (c.abs() * p_err + (coef_err * abs(scale))[:, None] * (one - self.p).abs()) + 4 * U * ref.abs()
-        out = torch.where(self.taken[:, None], ref, 0.0)
-        # a row without a coefficient is exactly zero
-        out = torch.where((coef == 0)[:, None], 0.0, out)
-        return out, torch.where(out == 0, 0.0, slack)
+        # a row that takes no part, or without a coefficient, is exactly zero
+        dead = (~self.taken | (coef == 0))[:, None]
+        return torch.where(dead, 0.0, ref), torch.where(dead, 0.0, slack)
 
 
 def policy(rows, old, ref, adv, weights, lo, hi, kl):
