@@ -124,9 +124,25 @@ struct SortKeys {
     int32_t wide_ids;
 };
 
-__device__ __forceinline__ uint32_t token_key(const SortKeys &s, int64_t i) {
-    const int64_t id = load_index(s.ids, s.wide_ids, i);
-    return static_cast<uint32_t>(id >= 0 && id < s.rows && id != s.padding_id ? id : s.rows);
+// Keys of tokens first, first + 64, ...: all loads are issued before the
+// first is used (tokens behind the last reload the last).
+template <int ROUNDS>
+__device__ __forceinline__ void token_keys(const SortKeys &s, int64_t first, int rounds, uint32_t (&key)[ROUNDS]) {
+    int64_t id[ROUNDS];
+    const int64_t last = s.n - 1;
+    if (s.wide_ids) {
+#pragma unroll
+        for (int r = 0; r < ROUNDS; ++r)
+            if (r < rounds) id[r] = gl(static_cast<const int64_t *>(s.ids))[first + r * 64 < last ? first + r * 64 : last];
+    } else {
+#pragma unroll
+        for (int r = 0; r < ROUNDS; ++r)
+            if (r < rounds) id[r] = gl(static_cast<const int32_t *>(s.ids))[first + r * 64 < last ? first + r * 64 : last];
+    }
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r)
+        key[r] = static_cast<uint32_t>(r < rounds && id[r] >= 0 && id[r] < s.rows && id[r] != s.padding_id ? id[r]
+                                                                                                         : s.rows);
 }
 
 // Among the lanes of a wave with `in` set: how many before this one have the
@@ -212,16 +228,19 @@ constexpr int SORT_SMALL_WAVES = SORT_SMALL_BLOCK / 64;
 constexpr int SORT_SMALL_ROUNDS = int(SORT_SMALL_MAX / SORT_SMALL_BLOCK);
 constexpr int SORT_SMALL_BITS = 9;
 
-// Clear the presence bits of table rows; part `part` of `parts`.
-__device__ __forceinline__ void clear_bits(uint32_t *present, int64_t rows, int64_t part, int64_t parts, int block) {
-    const int64_t words = (rows + 31) / 32;
-    for (int64_t i = part * block + threadIdx.x; i < words; i += parts * block) present[i] = 0;
+// Clear the flags of table rows; part `part` of `parts`.  A flag is a byte:
+// the tokens of one id all store the same 1, which needs no atomic.
+__device__ __forceinline__ void clear_flags(uint8_t *present, int64_t rows, int64_t part, int64_t parts, int block) {
+    const u32x4 z = {0, 0, 0, 0};
+    const int64_t chunks = (rows + 15) / 16;  // the array is padded to 256 bytes
+    for (int64_t i = part * block + threadIdx.x; i < chunks; i += parts * block)
+        gl(reinterpret_cast<u32x4 *>(present))[i] = z;
 }
 
 // The whole sort of up to SORT_SMALL_MAX tokens by one workgroup: the keys
 // stay in LDS between the passes.
 __global__ __launch_bounds__(SORT_SMALL_BLOCK) void sort_small(SortKeys s, int bits, int passes, uint32_t *keys_out,
-                                                               uint32_t *pos_out, uint32_t *present) {
+                                                               uint32_t *pos_out, uint8_t *present) {
     __shared__ uint32_t lkey[SORT_SMALL_MAX];
     __shared__ uint16_t lpos[SORT_SMALL_MAX];
     __shared__ uint32_t hist[SORT_SMALL_WAVES << SORT_SMALL_BITS];
@@ -229,41 +248,39 @@ __global__ __launch_bounds__(SORT_SMALL_BLOCK) void sort_small(SortKeys s, int b
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
     const int rounds = static_cast<int>((s.n + SORT_SMALL_BLOCK - 1) / SORT_SMALL_BLOCK);
     const int64_t first = int64_t(wave) * rounds * 64 + lane;
-    if (present) {
-        clear_bits(present, s.rows, 0, 1, SORT_SMALL_BLOCK);
-        __threadfence();  // the bits set at the end land on cleared words
-    }
+    if (present) clear_flags(present, s.rows, 0, 1, SORT_SMALL_BLOCK);
     uint32_t key[SORT_SMALL_ROUNDS];
     uint32_t pos[SORT_SMALL_ROUNDS];
+    if (s.n > 0) token_keys(s, first, rounds, key);
 #pragma unroll
-    for (int r = 0; r < SORT_SMALL_ROUNDS; ++r) {
-        const int64_t i = first + r * 64;
-        key[r] = r < rounds && i < s.n ? token_key(s, i) : 0;
-        pos[r] = static_cast<uint32_t>(i);
-    }
+    for (int r = 0; r < SORT_SMALL_ROUNDS; ++r) pos[r] = static_cast<uint32_t>(first + r * 64);
     const int bins = 1 << bits;
     Ranker<SORT_SMALL_WAVES, SORT_SMALL_ROUNDS> rk;
     for (int pass = 0; pass < passes; ++pass) {
         rk.count(key, rounds, first, s.n, pass * bits, bits, hist, bins);
         // thread b: digit b's keys over the waves, then over the digits
-        uint32_t mine = 0;
-        if (tid < bins)
-            for (int w = 0; w < SORT_SMALL_WAVES; ++w) {
-                const uint32_t c = hist[w * bins + tid];
-                hist[w * bins + tid] = mine;
-                mine += c;
-            }
+        uint32_t of[SORT_SMALL_WAVES], mine = 0;
+#pragma unroll
+        for (int w = 0; w < SORT_SMALL_WAVES; ++w) {
+            of[w] = tid < bins ? hist[w * bins + tid] : 0;
+            mine += of[w];
+        }
         uint32_t all;
-        const uint32_t base = block_scan<SORT_SMALL_WAVES>(mine, part, &all);
-        if (tid < bins)
-            for (int w = 0; w < SORT_SMALL_WAVES; ++w) hist[w * bins + tid] += base;
+        uint32_t at = block_scan<SORT_SMALL_WAVES>(mine, part, &all);
+        if (tid < bins) {
+#pragma unroll
+            for (int w = 0; w < SORT_SMALL_WAVES; ++w) {
+                hist[w * bins + tid] = at;
+                at += of[w];
+            }
+        }
         __syncthreads();
 #pragma unroll
         for (int r = 0; r < SORT_SMALL_ROUNDS; ++r) {
             if (r < rounds && first + r * 64 < s.n) {
-                const uint32_t at = hist[wave * bins + rk.digit[r]] + rk.rank[r];
-                lkey[at] = key[r];
-                lpos[at] = static_cast<uint16_t>(pos[r]);
+                const uint32_t to = hist[wave * bins + rk.digit[r]] + rk.rank[r];
+                lkey[to] = key[r];
+                lpos[to] = static_cast<uint16_t>(pos[r]);
             }
         }
         __syncthreads();
@@ -281,8 +298,8 @@ __global__ __launch_bounds__(SORT_SMALL_BLOCK) void sort_small(SortKeys s, int b
         if (r >= rounds || i >= s.n) continue;
         keys_out[i] = key[r];
         pos_out[i] = pos[r];
-        if (present && key[r] < static_cast<uint32_t>(s.rows) && (i == 0 || lkey[i - 1] != key[r]))
-            atomicOr(present + (key[r] >> 5), 1u << (key[r] & 31));
+        // after the barriers above every flag is cleared
+        if (present && key[r] < static_cast<uint32_t>(s.rows)) present[key[r]] = 1;
     }
 }
 
@@ -291,26 +308,41 @@ constexpr int SORT_WAVES = SORT_BLOCK / 64;
 constexpr int SORT_ROUNDS = int(SORT_TILE / SORT_BLOCK);
 constexpr int SORT_MAX_BINS = 1 << SORT_MAX_DIGIT_BITS;
 
+// Tiles up to which a tile finds its places from all tiles' counts by itself;
+// beyond, one workgroup sums the counts first.
+constexpr int64_t SORT_SELF_TILES = 256;
+
+// Keys and positions of a tile's tokens, wave by wave.
+template <bool FIRST>
+__device__ __forceinline__ void tile_keys(const SortKeys &s, int64_t first, uint32_t (&key)[SORT_ROUNDS]) {
+    if constexpr (FIRST) {
+        token_keys(s, first, SORT_ROUNDS, key);
+    } else {
+#pragma unroll
+        for (int r = 0; r < SORT_ROUNDS; ++r) key[r] = s.keys[first + r * 64 < s.n ? first + r * 64 : s.n - 1];
+    }
+}
+
 // Digit counts of tile blockIdx.x, as counts[digit * tiles + tile], so that
-// one exclusive sum over the array gives each tile its places.
+// one exclusive sum over the array gives each tile its places.  The first
+// pass clears the flags.
 template <bool FIRST>
 __global__ __launch_bounds__(SORT_BLOCK) void radix_count(SortKeys s, int shift, int bits, uint32_t *counts,
-                                                          uint32_t *present) {
+                                                          uint8_t *present) {
     __shared__ uint32_t hist[SORT_MAX_BINS];
     const int bins = 1 << bits;
+    const int64_t tiles = gridDim.x;
+    const int64_t first = int64_t(blockIdx.x) * SORT_TILE + int64_t(threadIdx.x >> 6) * SORT_ROUNDS * 64 + (threadIdx.x & 63);
+    uint32_t key[SORT_ROUNDS];
+    tile_keys<FIRST>(s, first, key);
     for (int i = threadIdx.x; i < bins; i += SORT_BLOCK) hist[i] = 0;
-    if (FIRST && present) clear_bits(present, s.rows, blockIdx.x, gridDim.x, SORT_BLOCK);
+    if (FIRST && present) clear_flags(present, s.rows, blockIdx.x, tiles, SORT_BLOCK);
     __syncthreads();
-    const int64_t begin = int64_t(blockIdx.x) * SORT_TILE;
-    for (int r = 0; r < SORT_ROUNDS; ++r) {
-        const int64_t i = begin + r * SORT_BLOCK + threadIdx.x;
-        if (i < s.n) {
-            const uint32_t key = FIRST ? token_key(s, i) : s.keys[i];
-            atomicAdd(&hist[(key >> shift) & (bins - 1)], 1u);
-        }
-    }
+#pragma unroll
+    for (int r = 0; r < SORT_ROUNDS; ++r)
+        if (first + r * 64 < s.n) atomicAdd(&hist[(key[r] >> shift) & (bins - 1)], 1u);
     __syncthreads();
-    for (int i = threadIdx.x; i < bins; i += SORT_BLOCK) counts[int64_t(i) * gridDim.x + blockIdx.x] = hist[i];
+    for (int i = threadIdx.x; i < bins; i += SORT_BLOCK) counts[i * tiles + blockIdx.x] = hist[i];
 }
 
 constexpr int SCAN_BLOCK = 1024;
@@ -335,28 +367,70 @@ __global__ __launch_bounds__(SCAN_BLOCK) void radix_scan(uint32_t *counts, int64
     }
 }
 
+// One pass of tile blockIdx.x: every key to its place.  `scanned`: counts
+// holds their exclusive sum already.
 template <bool FIRST>
 __global__ __launch_bounds__(SORT_BLOCK) void radix_scatter(SortKeys s, int shift, int bits, const uint32_t *counts,
-                                                            uint32_t *keys_out, uint32_t *pos_out) {
+                                                            int scanned, uint32_t *keys_out, uint32_t *pos_out,
+                                                            uint8_t *present) {
     __shared__ uint32_t hist[SORT_WAVES * SORT_MAX_BINS];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    __shared__ uint32_t part[SORT_WAVES];
+    constexpr int OWN = SORT_MAX_BINS / SORT_BLOCK;  // digits per thread
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
     const int bins = 1 << bits;
-    const int64_t first = int64_t(blockIdx.x) * SORT_TILE + int64_t(wave) * SORT_ROUNDS * 64 + lane;
+    const int64_t tiles = gridDim.x, tile = blockIdx.x;
+    const int64_t first = tile * SORT_TILE + int64_t(wave) * SORT_ROUNDS * 64 + lane;
     uint32_t key[SORT_ROUNDS], pos[SORT_ROUNDS];
+    tile_keys<FIRST>(s, first, key);
 #pragma unroll
     for (int r = 0; r < SORT_ROUNDS; ++r) {
         const int64_t i = first + r * 64;
-        key[r] = i < s.n ? (FIRST ? token_key(s, i) : s.keys[i]) : 0;
-        pos[r] = i < s.n ? (FIRST ? static_cast<uint32_t>(i) : s.pos[i]) : 0;
+        pos[r] = FIRST ? static_cast<uint32_t>(i) : s.pos[i < s.n ? i : s.n - 1];
+    }
+    // thread t owns digits OWN t, OWN t + 1: their first places of this tile
+    uint32_t place[OWN];
+    if (scanned) {
+#pragma unroll
+        for (int o = 0; o < OWN; ++o)
+            place[o] = tid * OWN + o < bins ? counts[(tid * OWN + o) * tiles + tile] : 0;
+    } else {
+        uint32_t before[OWN], of[OWN], sum = 0;
+#pragma unroll
+        for (int o = 0; o < OWN; ++o) {
+            before[o] = of[o] = 0;
+            if (tid * OWN + o < bins) {
+                const uint32_t *c = counts + (tid * OWN + o) * tiles;
+#pragma unroll 8
+                for (int64_t t = 0; t < tiles; ++t) {
+                    const uint32_t k = c[t];
+                    before[o] += t < tile ? k : 0;
+                    of[o] += k;
+                }
+            }
+            sum += of[o];
+        }
+        uint32_t all;
+        uint32_t at = block_scan<SORT_WAVES>(sum, part, &all);
+#pragma unroll
+        for (int o = 0; o < OWN; ++o) {
+            place[o] = at + before[o];
+            at += of[o];
+        }
     }
     Ranker<SORT_WAVES, SORT_ROUNDS> rk;
     rk.count(key, SORT_ROUNDS, first, s.n, shift, bits, hist, bins);
-    for (int b = threadIdx.x; b < bins; b += SORT_BLOCK) {
-        uint32_t at = counts[int64_t(b) * gridDim.x + blockIdx.x];
-        for (int w = 0; w < SORT_WAVES; ++w) {
-            const uint32_t c = hist[w * bins + b];
-            hist[w * bins + b] = at;
-            at += c;
+#pragma unroll
+    for (int o = 0; o < OWN; ++o) {
+        const int b = tid * OWN + o;
+        if (b < bins) {
+            uint32_t of[SORT_WAVES];
+#pragma unroll
+            for (int w = 0; w < SORT_WAVES; ++w) of[w] = hist[w * bins + b];
+#pragma unroll
+            for (int w = 0; w < SORT_WAVES; ++w) {
+                hist[w * bins + b] = place[o];
+                place[o] += of[w];
+            }
         }
     }
     __syncthreads();
@@ -366,17 +440,9 @@ __global__ __launch_bounds__(SORT_BLOCK) void radix_scatter(SortKeys s, int shif
             const uint32_t at = hist[wave * bins + rk.digit[r]] + rk.rank[r];
             keys_out[at] = key[r];
             pos_out[at] = pos[r];
+            if (FIRST && present && key[r] < static_cast<uint32_t>(s.rows)) present[key[r]] = 1;
         }
     }
-}
-
-// Set the presence bit of every key of a sorted list.
-__global__ __launch_bounds__(256) void mark_present(const uint32_t *keys, int64_t n, int64_t rows, uint32_t *present) {
-    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= n) return;
-    const uint32_t key = keys[i];
-    if (key < static_cast<uint32_t>(rows) && (i == 0 || keys[i - 1] != key))
-        atomicOr(present + (key >> 5), 1u << (key & 31));
 }
 
 // -------------------------------------------------------------- gradient --
@@ -385,7 +451,7 @@ struct SumArgs {
     const void *grad_out;
     void *table_grad;
     const uint32_t *keys, *pos;
-    const uint32_t *present;
+    const uint8_t *present;
     float *partials;
     int64_t grad_stride, table_stride, n, rows, dim, chunks;
     int32_t chunk, tiles;  // tokens per chunk; column tiles per row
@@ -419,47 +485,67 @@ __device__ __forceinline__ void write_row(const SumArgs &a, uint32_t key, int64_
     }
 }
 
-constexpr int SUM_UNROLL = 8;  // rows in flight per lane
+#ifndef RADAMW_SUM_UNROLL
+#define RADAMW_SUM_UNROLL 8
+#endif
+constexpr int SUM_UNROLL = RADAMW_SUM_UNROLL;  // rows in flight per lane
 
-// Columns [e, e + 8) of one chunk of the sorted tokens.
+// Values e .. dim - 1 (fewer than eight) of a row, zeros behind.
+template <int DT>
+__device__ __forceinline__ Raw8<DT> load_edge8(const void *p, int64_t e, int64_t dim) {
+    Raw8<DT> r;
+#pragma unroll
+    for (int c = 0; c < (DT == G_F32 ? 2 : 1); ++c) r.c[c] = u32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < 7; ++k) {
+        const uint32_t b = e + k < dim ? load_bits<DT>(p, e + k) : 0;
+        if constexpr (DT == G_F32) r.c[k >> 2][k & 3] = b;
+        else r.c[0][k >> 1] |= k & 1 ? b << 16 : b;
+    }
+    return r;
+}
+
+// Columns [e, e + 8) of one chunk of the sorted tokens.  The keys and
+// positions of a group of SUM_UNROLL tokens come in two wide loads (scalar
+// ones where a wave shares its chunk); entries behind the last token are read
+// and not used, and a token that takes no part reads row 0 in its place, so
+// that no load waits behind a branch.
 template <int GDT, int TDT, bool ACC>
 __device__ __forceinline__ void sum_chunk(const SumArgs &a, int64_t chunk, int64_t e) {
     const int64_t base = chunk * a.chunk;
     const int count = static_cast<int>(a.n - base < a.chunk ? a.n - base : a.chunk);
     const uint32_t *keys = a.keys + base, *pos = a.pos + base;
     const uint32_t rows = static_cast<uint32_t>(a.rows);
+    if (keys[0] >= rows) return;  // sorted behind every id that takes part
     const bool whole = e + 8 <= a.dim;
     bool continued = base > 0 && a.keys[base - 1] == keys[0];  // the first run began in an earlier chunk
     const bool more = base + count < a.n && a.keys[base + count] == keys[count - 1];
     f32x8 acc = 0.0f;
     for (int j0 = 0; j0 < count; j0 += SUM_UNROLL) {
-        uint32_t key[SUM_UNROLL + 1];
-        f32x8 v[SUM_UNROLL];
+        uint32_t key[SUM_UNROLL + 1], at[SUM_UNROLL];
+#pragma unroll
+        for (int u = 0; u <= SUM_UNROLL; ++u) key[u] = keys[j0 + u];
+#pragma unroll
+        for (int u = 0; u < SUM_UNROLL; ++u) at[u] = pos[j0 + u];
+#pragma unroll
+        for (int u = 0; u <= SUM_UNROLL; ++u) key[u] = j0 + u < count ? key[u] : 0xffffffffu;
         Raw8<GDT> raw[SUM_UNROLL];
+        const auto source = [&](int u) {
+            return static_cast<const char *>(a.grad_out) +
+                   int64_t(key[u] < rows ? at[u] : 0) * a.grad_stride * elem_bytes<GDT>;
+        };
+        if (whole) {
 #pragma unroll
-        for (int u = 0; u <= SUM_UNROLL; ++u) key[u] = j0 + u < count ? keys[j0 + u] : 0xffffffffu;
+            for (int u = 0; u < SUM_UNROLL; ++u) raw[u] = load_raw8<GDT>(source(u), e);
+        } else {
 #pragma unroll
-        for (int u = 0; u < SUM_UNROLL; ++u) {
-            if (key[u] < rows) {
-                const char *src = static_cast<const char *>(a.grad_out) +
-                                  int64_t(pos[j0 + u]) * a.grad_stride * elem_bytes<GDT>;
-                if (whole) {
-                    raw[u] = load_raw8<GDT>(src, e);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) v[u][k] = e + k < a.dim ? load_value<GDT>(src, e + k) : 0.0f;
-                }
-            }
+            for (int u = 0; u < SUM_UNROLL; ++u) raw[u] = load_edge8<GDT>(source(u), e, a.dim);
         }
 #pragma unroll
         for (int u = 0; u < SUM_UNROLL; ++u) {
-            if (key[u] >= rows) continue;
-            if (whole) {
+            if (key[u] >= rows) break;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) acc[k] += raw_value<GDT>(raw[u], k);
-            } else {
-                acc += v[u];
-            }
+            for (int k = 0; k < 8; ++k) acc[k] += raw_value<GDT>(raw[u], k);
             if (key[u + 1] != key[u]) {  // the run ends here, or crosses into the next chunk
                 const bool open = j0 + u + 1 == count && more;
                 if (!continued && !open) {
@@ -470,7 +556,7 @@ __device__ __forceinline__ void sum_chunk(const SumArgs &a, int64_t chunk, int64
                         store8<G_F32>(slot, e, acc);
                     } else {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
+                        for (int k = 0; k < 7; ++k)
                             if (e + k < a.dim) slot[e + k] = acc[k];
                     }
                 }
@@ -488,7 +574,7 @@ __device__ __forceinline__ void clear_rows(const SumArgs &a, int64_t block, int 
     const int64_t begin = block * a.rows_per_block;
     const int64_t end = begin + a.rows_per_block < a.rows ? begin + a.rows_per_block : a.rows;
     for (int64_t r = begin + (threadIdx.x >> lg); r < end; r += ROW_BLOCK >> lg) {
-        if ((a.present[r >> 5] >> (r & 31)) & 1) continue;
+        if (a.present[r]) continue;
         char *dst = static_cast<char *>(a.table_grad) + r * a.table_stride * elem_bytes<TDT>;
         for (int64_t e = int64_t(threadIdx.x & (lanes - 1)) * 8; e < a.dim; e += lanes * 8) {
             if (e + 8 <= a.dim) {
@@ -519,56 +605,85 @@ __global__ __launch_bounds__(ROW_BLOCK) void embedding_sum(SumArgs a, int lg) {
     }
 }
 
-// The runs that cross chunks: workgroup (c, tile) joins the run that begins
-// in chunk c and continues past it, 512 columns, the partial sums taken by
-// the four waves in turn and their sums added in the order of the waves.
+constexpr int JOIN_WAVES = ROW_BLOCK / 64;
+constexpr int JOIN_UNROLL = 4;
+// Partial sums up to which one wave joins a run by itself.
+constexpr int64_t JOIN_ALONE = 32;
+
+// Partial sum i of the run that begins in chunk c, columns [e, e + 8).
+__device__ __forceinline__ Raw8<G_F32> load_partial8(const SumArgs &a, int64_t c, int64_t i, int64_t e) {
+    const float *slot = a.partials + (i == 0 ? 2 * c + 1 : 2 * (c + i)) * a.dim;
+    return e + 8 <= a.dim ? load_raw8<G_F32>(slot, e) : load_edge8<G_F32>(slot, e, a.dim);
+}
+
+// Sum of partial sums first, first + step, ... up to `last`, in that order.
+__device__ __forceinline__ f32x8 sum_partials(const SumArgs &a, int64_t c, int64_t first, int64_t step, int64_t last,
+                                              int64_t e) {
+    f32x8 acc = 0.0f;
+    for (int64_t i = first; i <= last; i += step * JOIN_UNROLL) {
+        Raw8<G_F32> r[JOIN_UNROLL];
+#pragma unroll
+        for (int u = 0; u < JOIN_UNROLL; ++u) r[u] = load_partial8(a, c, i + u * step <= last ? i + u * step : last, e);
+#pragma unroll
+        for (int u = 0; u < JOIN_UNROLL; ++u)
+            if (i + u * step <= last)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) acc[k] += raw_value<G_F32>(r[u], k);
+    }
+    return acc;
+}
+
+// The runs that cross chunks: wave (c, tile) joins the run that begins in
+// chunk c and continues past it, 512 columns, in the order of the chunks.  A
+// long run is left to the whole workgroup, whose waves take its partial sums
+// in turn and add their sums in the order of the waves.
 template <int TDT, bool ACC>
 __global__ __launch_bounds__(ROW_BLOCK) void embedding_join(SumArgs a) {
-    constexpr int WAVES = ROW_BLOCK / 64;
-    __shared__ float sums[WAVES][64 * 8];
-    const int64_t c = blockIdx.x;
-    const int64_t base = c * a.chunk, next = base + a.chunk;
-    if (next >= a.n) return;
-    const uint32_t key = a.keys[next];
-    if (key >= static_cast<uint32_t>(a.rows) || a.keys[next - 1] != key) return;
-    if (base > 0 && a.keys[base] == key && a.keys[base - 1] == key) return;  // began earlier
-    // chunks after c that the run reaches
+    __shared__ float sums[JOIN_WAVES][64 * 8];
+    __shared__ int64_t reaches[JOIN_WAVES];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    int64_t reach = 0;
-    for (;;) {
-        const int64_t k = next + (reach + lane) * a.chunk;
-        const uint64_t on = __ballot(k < a.n && a.keys[k < a.n ? k : 0] == key);
-        if (on != ~uint64_t(0)) {
-            reach += __builtin_ctzll(~on);
-            break;
-        }
-        reach += 64;
-    }
+    const int64_t c = int64_t(blockIdx.x) * JOIN_WAVES + wave;
+    const int64_t base = c * a.chunk, next = base + a.chunk;
     const int64_t e = (int64_t(blockIdx.y) * 64 + lane) * 8;
-    f32x8 acc = 0.0f;
-    if (e < a.dim) {
-        for (int64_t i = wave; i <= reach; i += WAVES) {
-            const float *slot = a.partials + (i == 0 ? 2 * c + 1 : 2 * (c + i)) * a.dim;
-            if (e + 8 <= a.dim) {
-                const Raw8<G_F32> r = load_raw8<G_F32>(slot, e);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) acc[k] += raw_value<G_F32>(r, k);
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (e + k < a.dim) acc[k] += slot[e + k];
+    int64_t reach = 0;  // chunks after c that a run beginning in c reaches
+    uint32_t key = 0;
+    if (next < a.n) {
+        key = a.keys[next];
+        const uint32_t end = a.keys[next - 1], begin = a.keys[base], before = a.keys[base > 0 ? base - 1 : 0];
+        const bool earlier = base > 0 && begin == key && before == key;
+        if (key < static_cast<uint32_t>(a.rows) && end == key && !earlier) {
+            for (;;) {
+                const int64_t k = next + (reach + lane) * a.chunk;
+                const uint64_t on = __ballot(k < a.n && a.keys[k < a.n ? k : 0] == key);
+                if (on != ~uint64_t(0)) {
+                    reach += __builtin_ctzll(~on);
+                    break;
+                }
+                reach += 64;
             }
         }
     }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) sums[wave][k * 64 + lane] = acc[k];
+    if (reach > 0 && reach < JOIN_ALONE && e < a.dim) write_row<TDT, ACC>(a, key, e, sum_partials(a, c, 0, 1, reach, e));
+    if (lane == 0) reaches[wave] = reach;
     __syncthreads();
-    if (wave != 0 || e >= a.dim) return;
+    for (int w = 0; w < JOIN_WAVES; ++w) {
+        const int64_t far = reaches[w];
+        if (far < JOIN_ALONE) continue;  // the same for every wave
+        const int64_t of = c - wave + w;
+        f32x8 acc = 0.0f;
+        if (e < a.dim) acc = sum_partials(a, of, wave, JOIN_WAVES, far, e);
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w)
+        for (int k = 0; k < 8; ++k) sums[wave][k * 64 + lane] = acc[k];
+        __syncthreads();
+        if (wave == w && e < a.dim) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) acc[k] += sums[w][k * 64 + lane];
-    write_row<TDT, ACC>(a, key, e, acc);
+            for (int v = 0; v < JOIN_WAVES; ++v)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) acc[k] = v == 0 ? sums[0][k * 64 + lane] : acc[k] + sums[v][k * 64 + lane];
+            write_row<TDT, ACC>(a, key, e, acc);
+        }
+        __syncthreads();
+    }
 }
 
 // ------------------------------------------------------------- launchers --
@@ -581,16 +696,22 @@ EmbeddingPlan embedding_plan(int64_t n, int64_t rows, int64_t dim) {
         at += (bytes + 255) / 256 * 256;
         return here;
     };
+#ifdef RADAMW_CHUNK
+    p.chunk = RADAMW_CHUNK;
+#else
     p.chunk = n < 4096 ? 8 : n < 32768 ? 16 : 32;
+#endif
     p.chunks = (n + p.chunk - 1) / p.chunk;
-    p.keys[0] = take(n * 4);
-    p.pos[0] = take(n * 4);
+    // the sums read whole groups of SUM_UNROLL keys and positions, and one key behind
+    const int64_t list = (n + SUM_UNROLL + 1) * 4;
+    p.keys[0] = take(list);
+    p.pos[0] = take(list);
     if (n > SORT_SMALL_MAX) {
-        p.keys[1] = take(n * 4);
-        p.pos[1] = take(n * 4);
+        p.keys[1] = take(list);
+        p.pos[1] = take(list);
         p.counts = take((n + SORT_TILE - 1) / SORT_TILE * SORT_MAX_BINS * 4);
     }
-    p.present = take((rows + 31) / 32 * 4);
+    p.present = take(rows);
     p.partials = take(p.chunks * 2 * dim * 4);
     p.bytes = at;
     const int64_t pieces = (dim + 7) / 8;
@@ -608,7 +729,7 @@ EmbeddingPlan embedding_plan(int64_t n, int64_t rows, int64_t dim) {
 
 template <int GDT, int TDT>
 static hipError_t launch_sums(const SumArgs &a, int lg, dim3 grid, hipStream_t stream, int *launched) {
-    const dim3 join(static_cast<unsigned>(a.chunks), static_cast<unsigned>((a.dim + 511) / 512)), block(ROW_BLOCK);
+    const dim3 join(static_cast<unsigned>((a.chunks + JOIN_WAVES - 1) / JOIN_WAVES), static_cast<unsigned>((a.dim + 511) / 512)), block(ROW_BLOCK);
     if (a.accumulate) hipLaunchKernelGGL((embedding_sum<GDT, TDT, true>), grid, block, 0, stream, a, lg);
     else hipLaunchKernelGGL((embedding_sum<GDT, TDT, false>), grid, block, 0, stream, a, lg);
     hipError_t e = hipGetLastError();
@@ -634,13 +755,13 @@ static hipError_t launch_sums_to(const SumArgs &a, int tgdt, int lg, dim3 grid, 
 hipError_t launch_embedding_grad(const EmbeddingGradArgs &g, const EmbeddingPlan &p, int gdt, int tgdt,
                                  hipStream_t stream, int *launched) {
     auto words = [&](int64_t off) { return reinterpret_cast<uint32_t *>(g.workspace + off); };
-    uint32_t *present = g.accumulate ? nullptr : words(p.present);
+    uint8_t *present = g.accumulate ? nullptr : reinterpret_cast<uint8_t *>(g.workspace + p.present);
     SortKeys s{g.ids, nullptr, nullptr, g.n, g.rows, g.padding_id, g.wide_ids};
     const int key_bits = log2_ceil(g.rows + 1);
     hipError_t e;
     int at = 0;  // the buffer that holds the sorted keys
     if (g.n <= SORT_SMALL_MAX) {
-        const int passes = key_bits <= SORT_SMALL_BITS ? 1 : (key_bits + SORT_SMALL_BITS - 1) / SORT_SMALL_BITS;
+        const int passes = (key_bits + SORT_SMALL_BITS - 1) / SORT_SMALL_BITS;
         const int bits = (key_bits + passes - 1) / passes;
         hipLaunchKernelGGL(sort_small, dim3(1), dim3(SORT_SMALL_BLOCK), 0, stream, s, bits, passes, words(p.keys[0]),
                            words(p.pos[0]), present);
@@ -651,33 +772,31 @@ hipError_t launch_embedding_grad(const EmbeddingGradArgs &g, const EmbeddingPlan
         const int bits = (key_bits + passes - 1) / passes;
         const int64_t tiles = (g.n + SORT_TILE - 1) / SORT_TILE;
         const dim3 grid(static_cast<unsigned>(tiles)), block(SORT_BLOCK);
+        const int scanned = tiles > SORT_SELF_TILES;
         uint32_t *counts = words(p.counts);
         for (int pass = 0; pass < passes; ++pass) {
-            const int to = pass & 1;
             const int shift = pass * bits;
+            at = pass & 1;
             if (pass == 0)
                 hipLaunchKernelGGL(radix_count<true>, grid, block, 0, stream, s, shift, bits, counts, present);
             else hipLaunchKernelGGL(radix_count<false>, grid, block, 0, stream, s, shift, bits, counts, present);
             if ((e = hipGetLastError()) != hipSuccess) return e;
-            hipLaunchKernelGGL(radix_scan, dim3(1), dim3(SCAN_BLOCK), 0, stream, counts, tiles << bits);
-            if ((e = hipGetLastError()) != hipSuccess) return e;
+            ++*launched;
+            if (scanned) {
+                hipLaunchKernelGGL(radix_scan, dim3(1), dim3(SCAN_BLOCK), 0, stream, counts, tiles << bits);
+                if ((e = hipGetLastError()) != hipSuccess) return e;
+                ++*launched;
+            }
             if (pass == 0)
-                hipLaunchKernelGGL(radix_scatter<true>, grid, block, 0, stream, s, shift, bits, counts,
-                                   words(p.keys[to]), words(p.pos[to]));
+                hipLaunchKernelGGL(radix_scatter<true>, grid, block, 0, stream, s, shift, bits, counts, scanned,
+                                   words(p.keys[at]), words(p.pos[at]), present);
             else
-                hipLaunchKernelGGL(radix_scatter<false>, grid, block, 0, stream, s, shift, bits, counts,
-                                   words(p.keys[to]), words(p.pos[to]));
-            if ((e = hipGetLastError()) != hipSuccess) return e;
-            *launched += 3;
-            s.keys = words(p.keys[to]);
-            s.pos = words(p.pos[to]);
-            at = to;
-        }
-        if (present) {
-            hipLaunchKernelGGL(mark_present, dim3(static_cast<unsigned>((g.n + 255) / 256)), dim3(256), 0, stream,
-                               words(p.keys[at]), g.n, g.rows, present);
+                hipLaunchKernelGGL(radix_scatter<false>, grid, block, 0, stream, s, shift, bits, counts, scanned,
+                                   words(p.keys[at]), words(p.pos[at]), present);
             if ((e = hipGetLastError()) != hipSuccess) return e;
             ++*launched;
+            s.keys = words(p.keys[at]);
+            s.pos = words(p.pos[at]);
         }
     }
     SumArgs a{};

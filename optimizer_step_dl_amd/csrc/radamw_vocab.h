@@ -41,8 +41,8 @@ constexpr int SORT_MAX_DIGIT_BITS = 10;
 // Workspace of an embedding gradient over n tokens (byte offsets).
 struct EmbeddingPlan {
     int64_t keys[2], pos[2];  // two buffers each of sorted ids and token positions (u32)
-    int64_t counts;           // digit counts of the tiled sort (u32)
-    int64_t present;          // one bit per table row (u32 words)
+    int64_t counts;           // digit counts of the tiled sort's passes (u32)
+    int64_t present;          // one byte per table row
     int64_t partials;         // FP32 sums of runs that cross a chunk: [chunks][2][dim]
     int64_t bytes;
     int32_t chunk;            // sorted tokens per chunk
