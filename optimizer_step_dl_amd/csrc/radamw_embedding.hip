@@ -109,6 +109,57 @@ hipError_t launch_embedding_lookup(const LookupArgs &a, int tdt, int odt, hipStr
     }
 }
 
+// ------------------------------------------------------------- clearing --
+
+// Table rows to be cleared by the workgroups of a launch that sorts: sorting
+// is a few workgroups' latency, clearing all the others' bandwidth.
+struct ClearArgs {
+    void *table;
+    const uint8_t *present;  // rows to leave, or null: none
+    int64_t stride, dim;     // elements
+    int64_t begin, end;      // rows of this launch
+    int64_t rows_per_block;
+    int32_t dtype;
+    int32_t lg;              // 2^lg lanes share a row
+};
+
+// Values one clearing workgroup covers: 65536 measured 90.7 us for 32000 x
+// 4096 FP32 rows (5.8 TB/s), 32768 96 us, 16384 106 us.
+constexpr int64_t CLEAR_ELEMS = 65536;
+
+template <int TDT, int BLOCK>
+__device__ __forceinline__ void clear_rows_of(const ClearArgs &a, int64_t block) {
+    constexpr int E = chunk_elems<TDT>;
+    const int lanes = 1 << a.lg, per = BLOCK >> a.lg;  // rows at a time
+    const int mine = threadIdx.x >> a.lg, lane = threadIdx.x & 63;
+    const int64_t begin = a.begin + block * a.rows_per_block;
+    const int64_t end = begin + a.rows_per_block < a.end ? begin + a.rows_per_block : a.end;
+    const u32x4 z = {0, 0, 0, 0};
+    for (int64_t r0 = begin; r0 < end; r0 += 64) {
+        // the flags of 64 rows in one load
+        const int rows = static_cast<int>(end - r0 < 64 ? end - r0 : 64);
+        const uint64_t left = a.present ? __ballot(lane < rows && a.present[lane < rows ? r0 + lane : r0] != 0) : 0;
+        for (int r = mine; r < rows; r += per) {
+            if ((left >> r) & 1) continue;
+            char *dst = static_cast<char *>(a.table) + (r0 + r) * a.stride * elem_bytes<TDT>;
+            for (int64_t e = int64_t(threadIdx.x & (lanes - 1)) * E; e < a.dim; e += lanes * E) {
+                if (e + E <= a.dim) {
+                    stream_out<TDT>(dst, e, z);
+                } else {
+                    for (int64_t k = e; k < a.dim; ++k) store_value<TDT>(dst, k, 0.0f);
+                }
+            }
+        }
+    }
+}
+
+// Zeros have the same bits in both 16-bit types.
+template <int BLOCK>
+__device__ __forceinline__ void clear_rows(const ClearArgs &a, int64_t block) {
+    if (a.dtype == G_F32) clear_rows_of<G_F32, BLOCK>(a, block);
+    else clear_rows_of<G_BF16, BLOCK>(a, block);
+}
+
 // ------------------------------------------------------------------ sort --
 //
 // Least-significant-digit radix sort of (id, position), stable, so that
@@ -148,15 +199,19 @@ __device__ __forceinline__ void token_keys(const SortKeys &s, int64_t first, int
 // Among the lanes of a wave with `in` set: how many before this one have the
 // same digit, and how many have it at all.
 __device__ __forceinline__ void match_digit(uint32_t digit, int bits, bool in, int *before, int *total) {
-    uint64_t same = __ballot(in);
-    for (int b = 0; b < bits; ++b) {
-        const bool set = (digit >> b) & 1;
-        const uint64_t bal = __ballot(set);
-        same &= set ? bal : ~bal;
+    const uint64_t live = __ballot(in);
+    uint32_t lo = static_cast<uint32_t>(live), hi = static_cast<uint32_t>(live >> 32);
+#pragma unroll
+    for (int b = 0; b < SORT_MAX_DIGIT_BITS; ++b) {
+        if (b < bits) {
+            const uint32_t mine = static_cast<uint32_t>(static_cast<int32_t>(digit << (31 - b)) >> 31);  // 0 or ~0
+            const uint64_t set = __ballot(mine != 0);
+            lo &= ~(static_cast<uint32_t>(set) ^ mine);
+            hi &= ~(static_cast<uint32_t>(set >> 32) ^ mine);
+        }
     }
-    const uint64_t lower = (uint64_t(1) << (threadIdx.x & 63)) - 1;
-    *before = __popcll(same & lower);
-    *total = __popcll(same);
+    *before = __builtin_amdgcn_mbcnt_hi(hi, __builtin_amdgcn_mbcnt_lo(lo, 0));
+    *total = __builtin_popcount(lo) + __builtin_popcount(hi);
 }
 
 // Inclusive sum over the lanes of a wave.
@@ -223,60 +278,53 @@ struct Ranker {
     }
 };
 
-constexpr int SORT_SMALL_BLOCK = 1024;
-constexpr int SORT_SMALL_WAVES = SORT_SMALL_BLOCK / 64;
-constexpr int SORT_SMALL_ROUNDS = int(SORT_SMALL_MAX / SORT_SMALL_BLOCK);
 constexpr int SORT_SMALL_BITS = 9;
 
-// Clear the flags of table rows; part `part` of `parts`.  A flag is a byte:
-// the tokens of one id all store the same 1, which needs no atomic.
-__device__ __forceinline__ void clear_flags(uint8_t *present, int64_t rows, int64_t part, int64_t parts, int block) {
-    const u32x4 z = {0, 0, 0, 0};
-    const int64_t chunks = (rows + 15) / 16;  // the array is padded to 256 bytes
-    for (int64_t i = part * block + threadIdx.x; i < chunks; i += parts * block)
-        gl(reinterpret_cast<u32x4 *>(present))[i] = z;
-}
-
-// The whole sort of up to SORT_SMALL_MAX tokens by one workgroup: the keys
-// stay in LDS between the passes.
-__global__ __launch_bounds__(SORT_SMALL_BLOCK) void sort_small(SortKeys s, int bits, int passes, uint32_t *keys_out,
-                                                               uint32_t *pos_out, uint8_t *present) {
-    __shared__ uint32_t lkey[SORT_SMALL_MAX];
-    __shared__ uint16_t lpos[SORT_SMALL_MAX];
-    __shared__ uint32_t hist[SORT_SMALL_WAVES << SORT_SMALL_BITS];
-    __shared__ uint32_t part[SORT_SMALL_WAVES];
+// The whole sort of up to BLOCK * ROUNDS tokens by workgroup 0: the keys stay
+// in LDS between the passes.  The other workgroups clear the table.
+template <int BLOCK, int ROUNDS>
+__global__ __launch_bounds__(BLOCK) void sort_small(SortKeys s, int bits, int passes, uint32_t *keys_out,
+                                                               uint32_t *pos_out, ClearArgs clear) {
+    constexpr int WAVES = BLOCK / 64;
+    if (blockIdx.x > 0) {
+        clear_rows<BLOCK>(clear, blockIdx.x - 1);
+        return;
+    }
+    __shared__ uint32_t lkey[BLOCK * ROUNDS];
+    __shared__ uint16_t lpos[BLOCK * ROUNDS];
+    __shared__ uint32_t hist[WAVES << SORT_SMALL_BITS];
+    __shared__ uint32_t part[WAVES];
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-    const int rounds = static_cast<int>((s.n + SORT_SMALL_BLOCK - 1) / SORT_SMALL_BLOCK);
+    const int rounds = static_cast<int>((s.n + BLOCK - 1) / BLOCK);
     const int64_t first = int64_t(wave) * rounds * 64 + lane;
-    if (present) clear_flags(present, s.rows, 0, 1, SORT_SMALL_BLOCK);
-    uint32_t key[SORT_SMALL_ROUNDS];
-    uint32_t pos[SORT_SMALL_ROUNDS];
+    uint32_t key[ROUNDS];
+    uint32_t pos[ROUNDS];
     if (s.n > 0) token_keys(s, first, rounds, key);
 #pragma unroll
-    for (int r = 0; r < SORT_SMALL_ROUNDS; ++r) pos[r] = static_cast<uint32_t>(first + r * 64);
+    for (int r = 0; r < ROUNDS; ++r) pos[r] = static_cast<uint32_t>(first + r * 64);
     const int bins = 1 << bits;
-    Ranker<SORT_SMALL_WAVES, SORT_SMALL_ROUNDS> rk;
+    Ranker<WAVES, ROUNDS> rk;
     for (int pass = 0; pass < passes; ++pass) {
         rk.count(key, rounds, first, s.n, pass * bits, bits, hist, bins);
         // thread b: digit b's keys over the waves, then over the digits
-        uint32_t of[SORT_SMALL_WAVES], mine = 0;
+        uint32_t of[WAVES], mine = 0;
 #pragma unroll
-        for (int w = 0; w < SORT_SMALL_WAVES; ++w) {
+        for (int w = 0; w < WAVES; ++w) {
             of[w] = tid < bins ? hist[w * bins + tid] : 0;
             mine += of[w];
         }
         uint32_t all;
-        uint32_t at = block_scan<SORT_SMALL_WAVES>(mine, part, &all);
+        uint32_t at = block_scan<WAVES>(mine, part, &all);
         if (tid < bins) {
 #pragma unroll
-            for (int w = 0; w < SORT_SMALL_WAVES; ++w) {
+            for (int w = 0; w < WAVES; ++w) {
                 hist[w * bins + tid] = at;
                 at += of[w];
             }
         }
         __syncthreads();
 #pragma unroll
-        for (int r = 0; r < SORT_SMALL_ROUNDS; ++r) {
+        for (int r = 0; r < ROUNDS; ++r) {
             if (r < rounds && first + r * 64 < s.n) {
                 const uint32_t to = hist[wave * bins + rk.digit[r]] + rk.rank[r];
                 lkey[to] = key[r];
@@ -285,7 +333,7 @@ __global__ __launch_bounds__(SORT_SMALL_BLOCK) void sort_small(SortKeys s, int b
         }
         __syncthreads();
 #pragma unroll
-        for (int r = 0; r < SORT_SMALL_ROUNDS; ++r) {
+        for (int r = 0; r < ROUNDS; ++r) {
             if (r < rounds && first + r * 64 < s.n) {
                 key[r] = lkey[first + r * 64];
                 pos[r] = lpos[first + r * 64];
@@ -293,13 +341,11 @@ __global__ __launch_bounds__(SORT_SMALL_BLOCK) void sort_small(SortKeys s, int b
         }
     }
 #pragma unroll
-    for (int r = 0; r < SORT_SMALL_ROUNDS; ++r) {
+    for (int r = 0; r < ROUNDS; ++r) {
         const int64_t i = first + r * 64;
         if (r >= rounds || i >= s.n) continue;
         keys_out[i] = key[r];
         pos_out[i] = pos[r];
-        // after the barriers above every flag is cleared
-        if (present && key[r] < static_cast<uint32_t>(s.rows)) present[key[r]] = 1;
     }
 }
 
@@ -323,24 +369,38 @@ __device__ __forceinline__ void tile_keys(const SortKeys &s, int64_t first, uint
     }
 }
 
+// One byte per table row: 0 until the first pass's counts have seen a token
+// of it.  The tokens of one id all store the same 1, which needs no atomic.
+__global__ __launch_bounds__(256) void clear_flags(uint8_t *present, int64_t rows) {
+    const u32x4 z = {0, 0, 0, 0};
+    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    if (i * 16 < rows) gl(reinterpret_cast<u32x4 *>(present))[i] = z;  // the array is padded to 256 bytes
+}
+
 // Digit counts of tile blockIdx.x, as counts[digit * tiles + tile], so that
 // one exclusive sum over the array gives each tile its places.  The first
-// pass clears the flags.
+// pass sets the flags; workgroups behind the tiles clear table rows.
 template <bool FIRST>
-__global__ __launch_bounds__(SORT_BLOCK) void radix_count(SortKeys s, int shift, int bits, uint32_t *counts,
-                                                          uint8_t *present) {
+__global__ __launch_bounds__(SORT_BLOCK) void radix_count(SortKeys s, int shift, int bits, int64_t tiles,
+                                                          uint32_t *counts, uint8_t *present, ClearArgs clear) {
     __shared__ uint32_t hist[SORT_MAX_BINS];
+    if (blockIdx.x >= tiles) {
+        clear_rows<SORT_BLOCK>(clear, blockIdx.x - tiles);
+        return;
+    }
     const int bins = 1 << bits;
-    const int64_t tiles = gridDim.x;
     const int64_t first = int64_t(blockIdx.x) * SORT_TILE + int64_t(threadIdx.x >> 6) * SORT_ROUNDS * 64 + (threadIdx.x & 63);
     uint32_t key[SORT_ROUNDS];
     tile_keys<FIRST>(s, first, key);
     for (int i = threadIdx.x; i < bins; i += SORT_BLOCK) hist[i] = 0;
-    if (FIRST && present) clear_flags(present, s.rows, blockIdx.x, tiles, SORT_BLOCK);
     __syncthreads();
 #pragma unroll
-    for (int r = 0; r < SORT_ROUNDS; ++r)
-        if (first + r * 64 < s.n) atomicAdd(&hist[(key[r] >> shift) & (bins - 1)], 1u);
+    for (int r = 0; r < SORT_ROUNDS; ++r) {
+        if (first + r * 64 < s.n) {
+            atomicAdd(&hist[(key[r] >> shift) & (bins - 1)], 1u);
+            if (FIRST && present && key[r] < static_cast<uint32_t>(s.rows)) present[key[r]] = 1;
+        }
+    }
     __syncthreads();
     for (int i = threadIdx.x; i < bins; i += SORT_BLOCK) counts[i * tiles + blockIdx.x] = hist[i];
 }
@@ -370,15 +430,19 @@ __global__ __launch_bounds__(SCAN_BLOCK) void radix_scan(uint32_t *counts, int64
 // One pass of tile blockIdx.x: every key to its place.  `scanned`: counts
 // holds their exclusive sum already.
 template <bool FIRST>
-__global__ __launch_bounds__(SORT_BLOCK) void radix_scatter(SortKeys s, int shift, int bits, const uint32_t *counts,
-                                                            int scanned, uint32_t *keys_out, uint32_t *pos_out,
-                                                            uint8_t *present) {
+__global__ __launch_bounds__(SORT_BLOCK) void radix_scatter(SortKeys s, int shift, int bits, int64_t tiles,
+                                                            const uint32_t *counts, int scanned, uint32_t *keys_out,
+                                                            uint32_t *pos_out, ClearArgs clear) {
     __shared__ uint32_t hist[SORT_WAVES * SORT_MAX_BINS];
     __shared__ uint32_t part[SORT_WAVES];
+    if (blockIdx.x >= tiles) {
+        clear_rows<SORT_BLOCK>(clear, blockIdx.x - tiles);
+        return;
+    }
     constexpr int OWN = SORT_MAX_BINS / SORT_BLOCK;  // digits per thread
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
     const int bins = 1 << bits;
-    const int64_t tiles = gridDim.x, tile = blockIdx.x;
+    const int64_t tile = blockIdx.x;
     const int64_t first = tile * SORT_TILE + int64_t(wave) * SORT_ROUNDS * 64 + lane;
     uint32_t key[SORT_ROUNDS], pos[SORT_ROUNDS];
     tile_keys<FIRST>(s, first, key);
@@ -440,7 +504,6 @@ __global__ __launch_bounds__(SORT_BLOCK) void radix_scatter(SortKeys s, int shif
             const uint32_t at = hist[wave * bins + rk.digit[r]] + rk.rank[r];
             keys_out[at] = key[r];
             pos_out[at] = pos[r];
-            if (FIRST && present && key[r] < static_cast<uint32_t>(s.rows)) present[key[r]] = 1;
         }
     }
 }
@@ -451,14 +514,11 @@ struct SumArgs {
     const void *grad_out;
     void *table_grad;
     const uint32_t *keys, *pos;
-    const uint8_t *present;
     float *partials;
     int64_t grad_stride, table_stride, n, rows, dim, chunks;
     int32_t chunk, tiles;  // tokens per chunk; column tiles per row
     int32_t accumulate;
     float scale;
-    int64_t sum_blocks;  // workgroups below this sum, the others clear absent rows
-    int64_t rows_per_block;
 };
 
 // v into columns [e, e + 8) of table row `key`, rounded once.
@@ -536,7 +596,7 @@ __device__ __forceinline__ void sum_chunk(const SumArgs &a, int64_t chunk, int64
         };
         if (whole) {
 #pragma unroll
-            for (int u = 0; u < SUM_UNROLL; ++u) raw[u] = load_raw8<GDT>(source(u), e);
+            for (int u = 0; u < SUM_UNROLL; ++u) raw[u] = stream_raw8<GDT>(source(u), e);
         } else {
 #pragma unroll
             for (int u = 0; u < SUM_UNROLL; ++u) raw[u] = load_edge8<GDT>(source(u), e, a.dim);
@@ -567,31 +627,8 @@ __device__ __forceinline__ void sum_chunk(const SumArgs &a, int64_t chunk, int64
     }
 }
 
-// Rows of the table that no token names: zeros.
-template <int TDT>
-__device__ __forceinline__ void clear_rows(const SumArgs &a, int64_t block, int lg) {
-    const int lanes = 1 << lg;
-    const int64_t begin = block * a.rows_per_block;
-    const int64_t end = begin + a.rows_per_block < a.rows ? begin + a.rows_per_block : a.rows;
-    for (int64_t r = begin + (threadIdx.x >> lg); r < end; r += ROW_BLOCK >> lg) {
-        if (a.present[r]) continue;
-        char *dst = static_cast<char *>(a.table_grad) + r * a.table_stride * elem_bytes<TDT>;
-        for (int64_t e = int64_t(threadIdx.x & (lanes - 1)) * 8; e < a.dim; e += lanes * 8) {
-            if (e + 8 <= a.dim) {
-                store8<TDT>(dst, e, f32x8(0.0f));
-            } else {
-                for (int64_t k = e; k < a.dim; ++k) store_value<TDT>(dst, k, 0.0f);
-            }
-        }
-    }
-}
-
 template <int GDT, int TDT, bool ACC>
 __global__ __launch_bounds__(ROW_BLOCK) void embedding_sum(SumArgs a, int lg) {
-    if (!ACC && blockIdx.x >= a.sum_blocks) {
-        clear_rows<TDT>(a, blockIdx.x - a.sum_blocks, lg < 6 ? lg : 8);
-        return;
-    }
     const int64_t unit = (int64_t(blockIdx.x) << (8 - lg)) + (threadIdx.x >> lg);
     if (lg == 6) {
         // a whole wave shares its chunk: ids and positions are scalar loads
@@ -696,11 +733,7 @@ EmbeddingPlan embedding_plan(int64_t n, int64_t rows, int64_t dim) {
         at += (bytes + 255) / 256 * 256;
         return here;
     };
-#ifdef RADAMW_CHUNK
-    p.chunk = RADAMW_CHUNK;
-#else
-    p.chunk = n < 4096 ? 8 : n < 32768 ? 16 : 32;
-#endif
+    p.chunk = n < 4096 ? 8 : n < 32768 ? 16 : n < 65536 ? 32 : 64;
     p.chunks = (n + p.chunk - 1) / p.chunk;
     // the sums read whole groups of SUM_UNROLL keys and positions, and one key behind
     const int64_t list = (n + SUM_UNROLL + 1) * 4;
@@ -720,10 +753,6 @@ EmbeddingPlan embedding_plan(int64_t n, int64_t rows, int64_t dim) {
     p.tiles = static_cast<int32_t>((pieces + 63) / 64);
     const int64_t units = p.lg == 6 ? p.chunks * p.tiles : p.chunks;
     p.sum_blocks = (units + (int64_t(1) << (8 - p.lg)) - 1) >> (8 - p.lg);
-    // about 64-128 KiB per clearing workgroup, and at most 2^20 of them
-    p.rows_per_block = dim >= 32768 ? 1 : 32768 / dim;
-    if (p.rows_per_block < (rows >> 20)) p.rows_per_block = (rows >> 20) + 1;
-    p.clear_blocks = (rows + p.rows_per_block - 1) / p.rows_per_block;
     return p;
 }
 
@@ -755,31 +784,78 @@ static hipError_t launch_sums_to(const SumArgs &a, int tgdt, int lg, dim3 grid, 
 hipError_t launch_embedding_grad(const EmbeddingGradArgs &g, const EmbeddingPlan &p, int gdt, int tgdt,
                                  hipStream_t stream, int *launched) {
     auto words = [&](int64_t off) { return reinterpret_cast<uint32_t *>(g.workspace + off); };
-    uint8_t *present = g.accumulate ? nullptr : reinterpret_cast<uint8_t *>(g.workspace + p.present);
     SortKeys s{g.ids, nullptr, nullptr, g.n, g.rows, g.padding_id, g.wide_ids};
     const int key_bits = log2_ceil(g.rows + 1);
+    const bool dense = !g.accumulate;
+    ClearArgs clear{};
+    clear.table = g.table_grad;
+    clear.stride = g.table_stride;
+    clear.dim = g.dim;
+    clear.dtype = tgdt;
+    const int piece_bits = log2_ceil((g.dim * (tgdt == G_F32 ? 4 : 2) + 15) / 16);
+    clear.lg = piece_bits > 8 ? 8 : piece_bits;
+    // Rows [begin, end) for one launch, CLEAR_ELEMS values per workgroup and at
+    // most 2^20 workgroups; returns how many that takes.
+    const auto take_rows = [&](int64_t begin, int64_t end) -> int64_t {
+        clear.begin = begin;
+        clear.end = end;
+        clear.rows_per_block = g.dim >= CLEAR_ELEMS ? 1 : CLEAR_ELEMS / g.dim;
+        if (clear.rows_per_block <= ((end - begin) >> 20)) clear.rows_per_block = ((end - begin) >> 20) + 1;
+        return dense ? (end - begin + clear.rows_per_block - 1) / clear.rows_per_block : 0;
+    };
     hipError_t e;
     int at = 0;  // the buffer that holds the sorted keys
     if (g.n <= SORT_SMALL_MAX) {
+        // every row is cleared while one workgroup sorts
         const int passes = (key_bits + SORT_SMALL_BITS - 1) / SORT_SMALL_BITS;
         const int bits = (key_bits + passes - 1) / passes;
-        hipLaunchKernelGGL(sort_small, dim3(1), dim3(SORT_SMALL_BLOCK), 0, stream, s, bits, passes, words(p.keys[0]),
-                           words(p.pos[0]), present);
+        const int64_t blocks = 1 + take_rows(0, g.rows);
+        const dim3 grid(static_cast<unsigned>(blocks));
+        if (g.n <= SORT_TINY_MAX)
+            hipLaunchKernelGGL((sort_small<256, SORT_TINY_MAX / 256>), grid, dim3(256), 0, stream, s, bits, passes,
+                               words(p.keys[0]), words(p.pos[0]), clear);
+        else
+            hipLaunchKernelGGL((sort_small<1024, SORT_SMALL_MAX / 1024>), grid, dim3(1024), 0, stream, s, bits, passes,
+                               words(p.keys[0]), words(p.pos[0]), clear);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         ++*launched;
     } else {
         const int passes = (key_bits + SORT_MAX_DIGIT_BITS - 1) / SORT_MAX_DIGIT_BITS;
         const int bits = (key_bits + passes - 1) / passes;
         const int64_t tiles = (g.n + SORT_TILE - 1) / SORT_TILE;
-        const dim3 grid(static_cast<unsigned>(tiles)), block(SORT_BLOCK);
+        const dim3 block(SORT_BLOCK);
         const int scanned = tiles > SORT_SELF_TILES;
         uint32_t *counts = words(p.counts);
+        uint8_t *present = dense ? reinterpret_cast<uint8_t *>(g.workspace + p.present) : nullptr;
+        if (dense) {
+            hipLaunchKernelGGL(clear_flags, dim3(static_cast<unsigned>((g.rows + 4095) / 4096)), dim3(256), 0, stream,
+                               present, g.rows);
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+            ++*launched;
+        }
+        clear.present = present;
+        // The absent rows are cleared in equal shares by the launches behind
+        // the first count, which finds them.
+        const int64_t shares = 2 * passes - 1;
+        int64_t share = 0;
+        const auto grid = [&](bool first) {
+            int64_t blocks = tiles;
+            if (!first) {
+                blocks += take_rows(g.rows * share / shares, g.rows * (share + 1) / shares);
+                ++share;
+            }
+            return dim3(static_cast<unsigned>(blocks));
+        };
         for (int pass = 0; pass < passes; ++pass) {
             const int shift = pass * bits;
             at = pass & 1;
+            const dim3 count_grid = grid(pass == 0);
             if (pass == 0)
-                hipLaunchKernelGGL(radix_count<true>, grid, block, 0, stream, s, shift, bits, counts, present);
-            else hipLaunchKernelGGL(radix_count<false>, grid, block, 0, stream, s, shift, bits, counts, present);
+                hipLaunchKernelGGL(radix_count<true>, count_grid, block, 0, stream, s, shift, bits, tiles, counts,
+                                   present, clear);
+            else
+                hipLaunchKernelGGL(radix_count<false>, count_grid, block, 0, stream, s, shift, bits, tiles, counts,
+                                   present, clear);
             if ((e = hipGetLastError()) != hipSuccess) return e;
             ++*launched;
             if (scanned) {
@@ -787,24 +863,25 @@ hipError_t launch_embedding_grad(const EmbeddingGradArgs &g, const EmbeddingPlan
                 if ((e = hipGetLastError()) != hipSuccess) return e;
                 ++*launched;
             }
+            const dim3 scatter_grid = grid(false);
             if (pass == 0)
-                hipLaunchKernelGGL(radix_scatter<true>, grid, block, 0, stream, s, shift, bits, counts, scanned,
-                                   words(p.keys[at]), words(p.pos[at]), present);
+                hipLaunchKernelGGL(radix_scatter<true>, scatter_grid, block, 0, stream, s, shift, bits, tiles, counts,
+                                   scanned, words(p.keys[at]), words(p.pos[at]), clear);
             else
-                hipLaunchKernelGGL(radix_scatter<false>, grid, block, 0, stream, s, shift, bits, counts, scanned,
-                                   words(p.keys[at]), words(p.pos[at]), present);
+                hipLaunchKernelGGL(radix_scatter<false>, scatter_grid, block, 0, stream, s, shift, bits, tiles, counts,
+                                   scanned, words(p.keys[at]), words(p.pos[at]), clear);
             if ((e = hipGetLastError()) != hipSuccess) return e;
             ++*launched;
             s.keys = words(p.keys[at]);
             s.pos = words(p.pos[at]);
         }
     }
+    if (p.chunks == 0) return hipSuccess;
     SumArgs a{};
     a.grad_out = g.grad_out;
     a.table_grad = g.table_grad;
     a.keys = words(p.keys[at]);
     a.pos = words(p.pos[at]);
-    a.present = present;
     a.partials = reinterpret_cast<float *>(g.workspace + p.partials);
     a.grad_stride = g.grad_stride;
     a.table_stride = g.table_stride;
@@ -816,10 +893,8 @@ hipError_t launch_embedding_grad(const EmbeddingGradArgs &g, const EmbeddingPlan
     a.accumulate = g.accumulate;
     a.scale = g.scale;
     a.tiles = p.tiles;
-    a.sum_blocks = p.sum_blocks;
-    a.rows_per_block = p.rows_per_block;
     const int lg = p.lg;
-    const dim3 grid(static_cast<unsigned>(p.sum_blocks + (present ? p.clear_blocks : 0)));
+    const dim3 grid(static_cast<unsigned>(p.sum_blocks));
     switch (gdt) {
     case G_F32: return launch_sums_to<G_F32>(a, tgdt, lg, grid, stream, launched);
     case G_F16: return launch_sums_to<G_F16>(a, tgdt, lg, grid, stream, launched);

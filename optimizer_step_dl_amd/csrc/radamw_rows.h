@@ -103,6 +103,13 @@ __device__ __forceinline__ Raw8<DT> load_raw8(const void *p, int64_t e) {
     return r;
 }
 template <int DT>
+__device__ __forceinline__ Raw8<DT> stream_raw8(const void *p, int64_t e) {
+    Raw8<DT> r;
+    r.c[0] = stream_chunk<DT>(p, e);
+    if constexpr (DT == G_F32) r.c[1] = stream_chunk<DT>(p, e + 4);
+    return r;
+}
+template <int DT>
 __device__ __forceinline__ float raw_value(const Raw8<DT> &r, int j) {
     if constexpr (DT == G_F32) return chunk_value<DT>(r.c[j >> 2], j & 3);
     else return chunk_value<DT>(r.c[0], j);

@@ -32,8 +32,10 @@ int64_t lookup_blocks(int64_t n, int64_t dim);
 hipError_t launch_embedding_lookup(const LookupArgs &a, int tdt, int odt, hipStream_t stream);
 
 // Tokens one workgroup sorts in LDS, in one launch; longer lists take the
-// tiled sort.
-constexpr int64_t SORT_SMALL_MAX = 8192;
+// tiled sort.  Up to SORT_TINY_MAX it has four waves, which wait less for one
+// another, else sixteen.
+constexpr int SORT_SMALL_MAX = 8192;
+constexpr int SORT_TINY_MAX = 1024;
 // Tokens of one tile of the tiled sort.
 constexpr int64_t SORT_TILE = 4096;
 constexpr int SORT_MAX_DIGIT_BITS = 10;
@@ -50,8 +52,6 @@ struct EmbeddingPlan {
     int32_t lg;               // 2^lg lanes own 8 columns each of one chunk's column tile
     int32_t tiles;            // column tiles per row
     int64_t sum_blocks;       // workgroups that sum
-    int64_t rows_per_block;   // table rows one clearing workgroup looks at
-    int64_t clear_blocks;
 };
 
 struct EmbeddingGradArgs {

@@ -161,8 +161,7 @@ int radamw_embedding_grad(const void *grad_out, radamw_dtype grad_dtype, int64_t
     if (rows == 0 || (n == 0 && accumulate)) return RADAMW_OK;
     const EmbeddingPlan plan = embedding_plan(n, rows, dim);
     if (workspace_bytes < plan.bytes) return RADAMW_ERR_RANGE;
-    if (plan.chunks > LAUNCH_MAX_BLOCKS || plan.sum_blocks + plan.clear_blocks > LAUNCH_MAX_BLOCKS)
-        return RADAMW_ERR_RANGE;
+    if (plan.chunks > LAUNCH_MAX_BLOCKS || plan.sum_blocks > LAUNCH_MAX_BLOCKS) return RADAMW_ERR_RANGE;
     int dev;
     if ((rc = stream_device(stream, &dev))) return rc;
     DeviceScope scope(dev);
