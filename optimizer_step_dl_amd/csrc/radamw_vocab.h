@@ -75,8 +75,8 @@ hipError_t launch_embedding_grad(const EmbeddingGradArgs &a, const EmbeddingPlan
 
 // Per-row record the losses keep for the backward pass.
 struct RowStats {
-    float max;        // largest logit
-    float inv_sum;    // 1 / sum of exp(x - max)
+    float max;        // a logit m near the largest
+    float inv_sum;    // 1 / sum of exponentials relative to m
     float coef;       // d total / d log-probability of the label
     float one_less_p; // 1 - probability of the label
 };

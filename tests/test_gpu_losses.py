@@ -201,6 +201,30 @@ def test_policy_masked_logits(dtype, vocab):
     assert g.isnan().any(1).cpu().tolist() == [False, False, False, True, True, True, False]
 
 
+@pytest.mark.parametrize("dtype,vocab", [(F32, 30_000), (BF16, 100_000), (F16, 12_000), (BF16, 140_000)])
+def test_policy_rows_whose_leading_columns_mislead(dtype, vocab):
+    """The first columns are masked (-inf or the lowest value), far below the
+    rest, or hold a value so small that the others' exponentials relative to
+    it leave FP32's range; large maxima on either side of 2^24."""
+    announce(f"policy leading columns {dtype} {vocab}")
+    lead = 9000
+    n = 7
+    x, labels, taken = make_rows(n, vocab, dtype, 17, share=1.0)
+    labels[:] = vocab - 5
+    x[0, :lead] = float("-inf")
+    x[1, :lead] = torch.finfo(dtype).min
+    x[2, :lead] = -3000.0
+    x[3, :lead] = -90.0
+    if dtype != F16:
+        x[4] += 2.0 ** 23
+        x[5, :lead] = -(2.0 ** 25)
+        x[6, lead:] += 2.0 ** 26
+    adv = torch.randn(n, generator=gen(18))
+    check_policy(x, labels, taken, None, adv, ra.policy_options())
+    bounds = [0, 4, n]
+    check_preference(x, labels, taken, bounds, torch.tensor([-40.0, -50.0]), ra.preference_options(0.1, 0.1))
+
+
 @pytest.mark.parametrize("vocab", [777, 140_001])
 def test_policy_absent_rows_may_hold_anything(vocab):
     """Rows that take no part: NaN logits, old and reference values, any
@@ -366,6 +390,18 @@ def test_preference_far_margins():
     assert loss[0] == 0 and abs(loss[1] - 1000) < 20 and bool(o["total"].isfinite())
     assert bool(g.isfinite().all()) and bool((g[[2, 5]] == 0).all()) and bool((g[[0, 3]] == 0).all())
     assert abs(float(g[1, labels[1]]) + float(1 - o["logp"][1].exp())) < 1e-5
+
+
+def test_preference_pair_of_weight_zero_may_hold_nan():
+    announce("preference nan pair")
+    x, labels, taken = make_rows(8, 300, BF16, 19, share=1.0)
+    x[2] = NAN
+    x[6, 7] = float("inf")
+    x[7] = float("-inf")
+    o, g, *_ = run_preference(x, labels, [0, 2, 4, 6, 8], torch.zeros(4), ra.preference_options(),
+                              torch.tensor([1.0, 0.0]))
+    assert bool(o["total"].isfinite()) and o["loss"].isnan().tolist() == [False, True]
+    assert bool(g.isfinite().all()) and bool((g[[2, 3, 6, 7]] == 0).all()) and bool((g[:2] != 0).any())
 
 
 def test_preference_in_place_and_differences():
