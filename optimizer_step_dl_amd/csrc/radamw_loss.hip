@@ -83,28 +83,44 @@ __device__ __forceinline__ u32x4 lowest_chunk() {
     return u32x4{w, w, w, w};
 }
 
-// The last, partial chunk of a row: `left` values at element e, -inf behind.
+// How a row is cut: chunks of 16 bytes that start on a cache line, and the
+// values before the first and behind the last of them (`edges`), one to a
+// lane.  A row of 16-bit values may start at any even address; 16-byte
+// accesses from an odd multiple of two bytes cost 17% of the fused loss
+// (4097 rows of 50001 FP16 logits: 157 us, against 134 us for 50000), those
+// from a cache line 6% less than from elsewhere (50048: 125 us).
 template <int DT>
-__device__ __forceinline__ u32x4 load_partial(const void *p, int64_t e, int left) {
-    constexpr int E = chunk_elems<DT>;
-    u32x4 c = lowest_chunk<DT>();
-#pragma unroll
-    for (int j = 0; j < E - 1; ++j) {
-        if (j < left) {
-            const uint32_t b = load_bits<DT>(p, e + j);
-            if constexpr (DT == G_F32) c[j] = b;
-            else c[j >> 1] = j & 1 ? (c[j >> 1] & 0xffffu) | b << 16 : (c[j >> 1] & 0xffff0000u) | b;
-        }
-    }
-    return c;
-}
+struct RowShape {
+    static constexpr int E = chunk_elems<DT>;
+    int head;      // values before the first chunk (fewer than 128 bytes)
+    int full;      // chunks
+    int tail_at;   // first value behind them
+    int vocab;
 
-template <int DT>
-__device__ __forceinline__ void store_partial(void *p, int64_t e, int left, const float *v) {
-#pragma unroll
-    for (int j = 0; j < chunk_elems<DT> - 1; ++j)
-        if (j < left) store_value<DT>(p, e + j, v[j]);
-}
+    __device__ __forceinline__ RowShape(const void *row, int64_t vocab_) {
+        vocab = static_cast<int>(vocab_);
+        const int off = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 127);
+        const int lead = ((128 - off) & 127) / elem_bytes<DT>;
+        head = lead < vocab ? lead : vocab;
+        full = (vocab - head) / E;
+        tail_at = head + full * E;
+    }
+    // Value number of chunk k's first value.
+    __device__ __forceinline__ int64_t chunk_at(int64_t k) const { return head + k * E; }
+    // The edge value lane t holds, or -1: the head from lane 0 on, the tail
+    // from lane 64 on.
+    __device__ __forceinline__ int edge(int t) const {
+        if (t < 64) return t < head ? t : -1;
+        const int e = tail_at + (t - 64);
+        return e < vocab ? e : -1;
+    }
+    // The lane (of a workgroup of nt) that stores value v.
+    __device__ __forceinline__ int lane_of(int64_t v, int nt) const {
+        if (v < head) return static_cast<int>(v);
+        if (v >= tail_at) return 64 + static_cast<int>(v - tail_at);
+        return static_cast<int>((v - head) / E) % nt;
+    }
+};
 
 template <int DT>
 __device__ __forceinline__ void store_values(void *p, int64_t e, const float *v) {
@@ -121,12 +137,11 @@ __device__ __forceinline__ void store_values(void *p, int64_t e, const float *v)
 // A row that takes no part: a gradient of zeros.
 template <int DT, int NT>
 __device__ __forceinline__ void zero_row(void *row, int64_t vocab) {
-    constexpr int E = chunk_elems<DT>;
     const u32x4 z = {0, 0, 0, 0};
-    const int64_t full = vocab / E;
-    for (int64_t k = threadIdx.x; k < full; k += NT) stream_out<DT>(row, k * E, z);
-    const int64_t e = full * E + threadIdx.x;
-    if (e < vocab) store_value<DT>(row, e, 0.0f);
+    const RowShape<DT> s(row, vocab);
+    for (int k = threadIdx.x; k < s.full; k += NT) stream_out<DT>(row, s.chunk_at(k), z);
+    const int e = s.edge(threadIdx.x);
+    if (e >= 0) store_value<DT>(row, e, 0.0f);
 }
 
 // What a row's own scalars give: formed by one wave.
@@ -329,28 +344,24 @@ __global__ __launch_bounds__(NT) void loss_rows(LogitsArgs x, ROW f) {
         return;
     }
     const char *in = static_cast<const char *>(x.logits) + row * x.stride * elem_bytes<DT>;
-    const int vocab = static_cast<int>(x.vocab), full = vocab / E, left = vocab % E;
-    const int used = (full + (left != 0) + NT - 1) / NT;  // chunks of the busiest lane
+    const RowShape<DT> s(in, x.vocab);
+    const int used = (s.full + NT - 1) / NT;  // chunks of the busiest lane
     const float at_label = load_value<DT>(in, label);
     u32x4 c[CH];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
         const int k = tid + i * NT;
-        if (k < full) c[i] = stream_chunk<DT>(in, int64_t(k) * E);
+        if (k < s.full) c[i] = stream_chunk<DT>(in, s.chunk_at(k));
         else c[i] = lowest_chunk<DT>();
     }
-    if (left && tid == full % NT) {
-        const u32x4 t = load_partial<DT>(in, int64_t(full) * E, left);
-#pragma unroll
-        for (int i = 0; i < CH; ++i)
-            if (i == full / NT) c[i] = t;
-    }
-    float top = -__builtin_inff();
+    const int edge = s.edge(tid);
+    const float at_edge = edge >= 0 ? load_value<DT>(in, edge) : -__builtin_inff();
+    float top = at_edge;
 #pragma unroll
     for (int j = 0; j < E; ++j) top = fmaxf(top, chunk_value<DT>(c[0], j));
     top = block_max<NT>(top, sh.tops);
     const float shift = top * LOG2E;
-    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float part[4] = {exp_shifted<!GRAD>(at_edge, shift), 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
         if (i < used) {
@@ -382,12 +393,12 @@ __global__ __launch_bounds__(NT) void loss_rows(LogitsArgs x, ROW f) {
                 float v[E];
 #pragma unroll
                 for (int j = 0; j < E; ++j) v[j] = exp_shifted<false>(chunk_value<DT>(c[i], j), shift) * k;
-                if (at < full) store_values<DT>(out, int64_t(at) * E, v);
-                else if (at == full && left) store_partial<DT>(out, int64_t(full) * E, left, v);
+                if (at < s.full) store_values<DT>(out, s.chunk_at(at), v);
             }
         }
-        // the label's value, behind its own lane's store of the chunk
-        if (tid == static_cast<int>(label / E) % NT) store_value<DT>(out, label, sh.at_label);
+        if (edge >= 0) store_value<DT>(out, edge, exp_shifted<false>(at_edge, shift) * k);
+        // the label's value, behind its own lane's store of what holds it
+        if (tid == s.lane_of(label, NT)) store_value<DT>(out, label, sh.at_label);
     }
 }
 
@@ -418,8 +429,7 @@ __global__ __launch_bounds__(STREAM_BLOCK) void loss_rows_long(LogitsArgs x, ROW
         return;
     }
     const char *in = static_cast<const char *>(x.logits) + row * x.stride * elem_bytes<DT>;
-    const int64_t full = x.vocab / E;
-    const int left = static_cast<int>(x.vocab % E);
+    const RowShape<DT> s(in, x.vocab);
     const float at_label = load_value<DT>(in, label);
     // top: the lane's largest value so far; shift: what its sum is relative
     // to.  A lane that holds something else than a number, or a value too
@@ -442,22 +452,23 @@ __global__ __launch_bounds__(STREAM_BLOCK) void loss_rows_long(LogitsArgs x, ROW
         top = t;
         shift = to;
     };
-    for (int64_t k0 = 0; k0 < full; k0 += NT * U) {
+    const int edge = s.edge(tid);
+    const float at_edge = edge >= 0 ? load_value<DT>(in, edge) : -__builtin_inff();
+    for (int k0 = 0; k0 < s.full; k0 += NT * U) {
         u32x4 c[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t k = k0 + u * NT + tid;
-            if (k < full) c[u] = GRAD ? load_chunk<DT>(in, k * E) : stream_chunk<DT>(in, k * E);
+            const int k = k0 + u * NT + tid;
+            if (k < s.full) c[u] = GRAD ? load_chunk<DT>(in, s.chunk_at(k)) : stream_chunk<DT>(in, s.chunk_at(k));
             else c[u] = lowest_chunk<DT>();
         }
         take(c);
     }
-    if (left && tid == 0) {
-        u32x4 c[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) c[u] = lowest_chunk<DT>();
-        c[0] = load_partial<DT>(in, full * E, left);
-        take(c);
+    if (edge >= 0) {
+        const float t = fmaxf(top, at_edge), to = shiftable(t) ? t * LOG2E : 0.0f;
+        sum = rescaled(sum, shift, to) + double(exp_shifted<!GRAD>(at_edge, to));
+        top = t;
+        shift = to;
     }
     const float all = block_max<NT>(top, sh.tops);
     if (!shiftable(all)) {
@@ -479,90 +490,75 @@ __global__ __launch_bounds__(STREAM_BLOCK) void loss_rows_long(LogitsArgs x, ROW
             zero_row<DT, NT>(out, x.vocab);
             return;
         }
-        for (int64_t k0 = 0; k0 < full; k0 += NT * U) {
+        for (int k0 = 0; k0 < s.full; k0 += NT * U) {
             u32x4 c[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int64_t at = k0 + u * NT + tid;
-                if (at < full) c[u] = stream_chunk<DT>(in, at * E);
+                const int at = k0 + u * NT + tid;
+                if (at < s.full) c[u] = stream_chunk<DT>(in, s.chunk_at(at));
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int64_t at = k0 + u * NT + tid;
-                if (at >= full) continue;
+                const int at = k0 + u * NT + tid;
+                if (at >= s.full) continue;
                 float v[E];
 #pragma unroll
                 for (int j = 0; j < E; ++j) v[j] = exp_shifted<false>(chunk_value<DT>(c[u], j), shift) * k;
-                store_values<DT>(out, at * E, v);
+                store_values<DT>(out, s.chunk_at(at), v);
             }
         }
-        if (left && full % NT == tid) {
-            const u32x4 c = load_partial<DT>(in, full * E, left);
-            float v[E];
-#pragma unroll
-            for (int j = 0; j < E; ++j) v[j] = exp_shifted<false>(chunk_value<DT>(c, j), shift) * k;
-            store_partial<DT>(out, full * E, left, v);
-        }
-        if (tid == static_cast<int>((label / E) % NT)) store_value<DT>(out, label, sh.at_label);
+        if (edge >= 0) store_value<DT>(out, edge, exp_shifted<false>(at_edge, shift) * k);
+        if (tid == s.lane_of(label, NT)) store_value<DT>(out, label, sh.at_label);
     }
 }
 
 // ------------------------------------------- gradient from saved records --
 
-// One chunk per lane and 1024 lanes: 574 us for 7847 rows of 131072 BF16
+// One chunk per lane and 1024 lanes measured 574 us for 7847 rows of 131072 BF16
 // logits, 5492 of them live (3.5 GB, 6.1 TB/s), against 616 us with two
 // chunks and 635 us with 256 lanes of four.
 constexpr int GRAD_BLOCK = 1024;
-constexpr int GRAD_UNROLL = 1;
 
-// Workgroup (row, part): GRAD_BLOCK * GRAD_UNROLL chunks of one row.
+// Workgroup (row, part): GRAD_BLOCK chunks of one row, part 0 its edges too.
 template <int DT>
 __global__ __launch_bounds__(GRAD_BLOCK) void logits_grad(LogitsArgs x, const float *upstream) {
     constexpr int E = chunk_elems<DT>;
     const int64_t row = blockIdx.x;
-    const int64_t first = int64_t(blockIdx.y) * GRAD_BLOCK * GRAD_UNROLL;
+    const int tid = threadIdx.x, at = static_cast<int>(blockIdx.y) * GRAD_BLOCK + tid;
     char *out = static_cast<char *>(x.grad) + row * x.grad_stride * elem_bytes<DT>;
     const char *in = static_cast<const char *>(x.logits) + row * x.stride * elem_bytes<DT>;
-    const int64_t full = x.vocab / E;
-    const int left = static_cast<int>(x.vocab % E);
-    const RowStats s = x.stats[row];
+    const RowShape<DT> s(in, x.vocab);
+    const RowStats r = x.stats[row];
     const float up = upstream ? *upstream : 1.0f;
-    const double g = double(s.coef) * double(x.grad_scale) * double(up);
+    const double g = double(r.coef) * double(x.grad_scale) * double(up);
     const int64_t label = load_index(x.labels, x.wide_ids, row);
     // no part in the loss (its record is all zeros), or clipped
-    const bool dead = s.coef == 0.0f || label < 0 || label >= x.vocab;
-    const float k = static_cast<float>(-g * double(s.inv_sum));
-    const float at_label = static_cast<float>(g * double(s.one_less_p));
+    const bool dead = r.coef == 0.0f || label < 0 || label >= x.vocab;
+    const float k = dead ? 0.0f : static_cast<float>(-g * double(r.inv_sum));
+    const float at_label = static_cast<float>(g * double(r.one_less_p));
     // x - m first where the forward pass summed so
-    if (!dead && !shiftable(s.max)) {
-        const int64_t end = first + GRAD_BLOCK * GRAD_UNROLL < full ? (first + GRAD_BLOCK * GRAD_UNROLL) * E : x.vocab;
-#pragma clang loop unroll(disable)
-        for (int64_t e = first * E + threadIdx.x; e < end; e += GRAD_BLOCK) {
-            const float v = exp_neg(load_value<DT>(in, e) - s.max) * k;
-            store_value<DT>(out, e, e == label ? at_label : v);
-        }
-        return;
+    const bool shifted = dead || shiftable(r.max);
+    const float shift = dead ? 0.0f : r.max * LOG2E;
+    const int edge = blockIdx.y == 0 ? s.edge(tid) : -1;
+    if (edge >= 0) {
+        const float z = dead ? -__builtin_inff() : load_value<DT>(in, edge);
+        const float v = (shifted ? exp_shifted<false>(z, shift) : exp_neg(z - r.max)) * k;
+        store_value<DT>(out, edge, !dead && edge == label ? at_label : v);
     }
-    const float shift = dead ? 0.0f : s.max * LOG2E;
-    u32x4 c[GRAD_UNROLL];
+    if (at >= s.full) return;
+    u32x4 c = lowest_chunk<DT>();  // exponentials of zero
+    if (!dead) c = stream_chunk<DT>(in, s.chunk_at(at));
+    float v[E];
+    if (shifted) {
 #pragma unroll
-    for (int u = 0; u < GRAD_UNROLL; ++u) {
-        const int64_t at = first + u * GRAD_BLOCK + threadIdx.x;
-        c[u] = lowest_chunk<DT>();  // exponentials of zero
-        if (!dead && at < full) c[u] = stream_chunk<DT>(in, at * E);
-        else if (!dead && at == full && left) c[u] = load_partial<DT>(in, full * E, left);
+        for (int j = 0; j < E; ++j) v[j] = exp_shifted<false>(chunk_value<DT>(c, j), shift) * k;
+    } else {
+#pragma unroll
+        for (int j = 0; j < E; ++j) v[j] = exp_neg(chunk_value<DT>(c, j) - r.max) * k;
     }
-    const float factor = dead ? 0.0f : k;
-#pragma unroll
-    for (int u = 0; u < GRAD_UNROLL; ++u) {
-        const int64_t at = first + u * GRAD_BLOCK + threadIdx.x;
-        float v[E];
-#pragma unroll
-        for (int j = 0; j < E; ++j) v[j] = exp_shifted<false>(chunk_value<DT>(c[u], j), shift) * factor;
-        if (at < full) store_values<DT>(out, at * E, v);
-        else if (at == full && left) store_partial<DT>(out, full * E, left, v);
-        if (!dead && at == label / E) store_value<DT>(out, label, at_label);
-    }
+    store_values<DT>(out, s.chunk_at(at), v);
+    // the label's value, behind its own lane's store of the chunk
+    if (!dead && label >= s.chunk_at(at) && label < s.chunk_at(at + 1)) store_value<DT>(out, label, at_label);
 }
 
 // ----------------------------------------------------------- small sums --
@@ -642,14 +638,23 @@ static hipError_t launch_rows(const LogitsArgs &x, const ROW &f, hipStream_t str
     const dim3 grid(static_cast<unsigned>(x.n));
 #define RADAMW_ROWS(NT, CH) \
     hipLaunchKernelGGL((loss_rows<DT, NT, CH, GRAD, ROW>), grid, dim3(NT), 0, stream, x, f)
-    if (!GRAD && chunks > 256 * 4)
-        hipLaunchKernelGGL((loss_rows_long<DT, GRAD, ROW>), grid, dim3(STREAM_BLOCK), 0, stream, x, f);
-    else if (chunks <= 256 * 4) RADAMW_ROWS(256, 4);
-    else if (chunks <= 256 * 8) RADAMW_ROWS(256, 8);
-    else if (chunks <= 256 * 16) RADAMW_ROWS(256, 16);
-    else if (chunks <= 512 * 16) RADAMW_ROWS(512, 16);
-    else if (chunks <= 1024 * 16) RADAMW_ROWS(1024, 16);
-    else hipLaunchKernelGGL((loss_rows_long<DT, GRAD, ROW>), grid, dim3(STREAM_BLOCK), 0, stream, x, f);
+#define RADAMW_LONG() \
+    hipLaunchKernelGGL((loss_rows_long<DT, GRAD, ROW>), grid, dim3(STREAM_BLOCK), 0, stream, x, f)
+    // Without a gradient nothing has to be held: a read that streams reaches
+    // 6.8 TB/s (5492 rows of 131072 BF16 logits: 212 us, against 362 us from
+    // registers, one workgroup per CU).  Short rows waste its 1024 lanes.
+    if (chunks <= 256 * 4) {
+        RADAMW_ROWS(256, 4);
+    } else if constexpr (!GRAD) {
+        RADAMW_LONG();
+    } else {
+        if (chunks <= 256 * 8) RADAMW_ROWS(256, 8);
+        else if (chunks <= 256 * 16) RADAMW_ROWS(256, 16);
+        else if (chunks <= 512 * 16) RADAMW_ROWS(512, 16);
+        else if (chunks <= 1024 * 16) RADAMW_ROWS(1024, 16);
+        else RADAMW_LONG();
+    }
+#undef RADAMW_LONG
 #undef RADAMW_ROWS
     return hipGetLastError();
 }
@@ -675,8 +680,8 @@ hipError_t launch_policy_loss(const PolicyArgs &a, int dt, hipStream_t stream, i
 
 hipError_t launch_logits_grad(const LogitsArgs &x, const float *upstream, int dt, hipStream_t stream) {
     const int64_t chunks = (x.vocab + (dt == G_F32 ? 3 : 7)) / (dt == G_F32 ? 4 : 8);
-    const int64_t per = int64_t(GRAD_BLOCK) * GRAD_UNROLL;
-    const dim3 grid(static_cast<unsigned>(x.n), static_cast<unsigned>((chunks + per - 1) / per)), block(GRAD_BLOCK);
+    const dim3 grid(static_cast<unsigned>(x.n), static_cast<unsigned>((chunks + GRAD_BLOCK - 1) / GRAD_BLOCK));
+    const dim3 block(GRAD_BLOCK);
     switch (dt) {
     case G_F32: hipLaunchKernelGGL(logits_grad<G_F32>, grid, block, 0, stream, x, upstream); break;
     case G_F16: hipLaunchKernelGGL(logits_grad<G_F16>, grid, block, 0, stream, x, upstream); break;
