@@ -837,7 +837,12 @@ def _row_values(t: Optional[torch.Tensor], what: str, n: int, dev_index: int):
     """Pointer of a contiguous FP32 tensor of n values, or None."""
     if t is None:
         return None
-    _check_fast(t, what, dev_index, n, torch.float32)
+    try:
+        good = t.dtype is torch.float32 and t.numel() == n and t.get_device() == dev_index and t.is_contiguous()
+    except AttributeError:
+        good = False
+    if not good:
+        _check_fast(t, what, dev_index, n, torch.float32)  # says what is wrong
     return t.data_ptr()
 
 

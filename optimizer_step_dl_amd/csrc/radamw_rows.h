@@ -127,6 +127,19 @@ __device__ __forceinline__ void store8(void *p, int64_t e, f32x8 v) {
     }
 }
 
+template <int DT>
+__device__ __forceinline__ void stream8(void *p, int64_t e, f32x8 v) {
+    if constexpr (DT == G_F32) {
+        const f32x4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
+        stream_out<DT>(p, e, __builtin_bit_cast(u32x4, lo));
+        stream_out<DT>(p, e + 4, __builtin_bit_cast(u32x4, hi));
+    } else if constexpr (DT == G_F16) {
+        stream_out<DT>(p, e, __builtin_bit_cast(u32x4, __builtin_convertvector(v, f16x8)));
+    } else {
+        stream_out<DT>(p, e, __builtin_bit_cast(u32x4, __builtin_convertvector(v, bf16x8)));
+    }
+}
+
 // Entry i of an index array, as 64 bits.
 __device__ __forceinline__ int64_t load_index(const void *p, int32_t wide, int64_t i) {
     return wide ? gl(static_cast<const int64_t *>(p))[i] : int64_t(gl(static_cast<const int32_t *>(p))[i]);

@@ -26,8 +26,7 @@ struct LookupArgs {
     float scale;
     int32_t wide_ids;  // 0: int32, 1: int64
 };
-// Lanes (as a power of two) per row, and the workgroups of a lookup.
-int lookup_lanes_log2(int64_t dim);
+// Workgroups (along x) of a lookup.
 int64_t lookup_blocks(int64_t n, int64_t dim);
 hipError_t launch_embedding_lookup(const LookupArgs &a, int tdt, int odt, hipStream_t stream);
 

@@ -377,6 +377,21 @@ def test_preference_sequences(bounds, index):
     assert bool((g[:bounds[0]] == 0).all()) and bool((g[bounds[-1]:] == 0).all())
 
 
+@pytest.mark.parametrize("pairs", [1, 2, 8, 9, 40, 1100])
+def test_preference_pair_counts(pairs):
+    """One workgroup for up to 8 pairs, one each beyond, with and without weights."""
+    announce(f"preference pairs={pairs}")
+    g = gen(pairs)
+    lengths = torch.randint(0, 6, (2 * pairs,), generator=g)
+    bounds = [2] + (2 + lengths.cumsum(0)).tolist()
+    x, labels, taken = make_rows(bounds[-1] + 3, 33, F32, pairs)
+    r = Rows(x, labels, taken)
+    sums = preference(r, bounds, torch.zeros(2 * pairs), None, 0.1, 0.0)[2].float()
+    ref = sums + 3 * torch.randn(2 * pairs, generator=g)
+    check_preference(x, labels, taken, bounds, ref, ra.preference_options(0.3, 0.2))
+    check_preference(x, labels, taken, bounds, ref, ra.preference_options(0.3, 0.0), torch.rand(pairs, generator=g))
+
+
 def test_preference_far_margins():
     """h of +-1000: the loss is linear or zero, without overflow; weight 0."""
     announce("preference margins")
