@@ -774,28 +774,22 @@ def radamw_lists_fused_step(lists: Sequence[TensorList], steps: Sequence[int], o
 
 # ------------------------------------------------------ vocabulary operators --
 
-class _Here:
-    """The device scope of a call whose device is the current one already:
-    nothing to switch (torch's own scope costs about a microsecond)."""
-
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *exc):
-        return False
-
-
-_HERE_SCOPE = _Here()
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _scope(device: torch.device):
-    return _HERE_SCOPE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-
-def _queue(device: torch.device):
-    """_stream without the Stream object around the handle."""
-    return _raw_stream(device.index) if _raw_stream is not None else _stream(device)
+def _submit(where: str, entry, device: torch.device, *args) -> None:
+    """Call a C entry point on the device's current stream, its last
+    argument.  Device scope and stream object (3 us together) are left out
+    where the device is the current one."""
+    i = device.index
+    if _raw_stream is not None and _current_device() == i:
+        rc = entry(*args, _raw_stream(i))
+    else:
+        with torch.cuda.device(device):
+            rc = entry(*args, _stream(device))
+    if rc != RADAMW_OK:
+        raise RadamwError(rc, where)
 
 
 def _rows2d(t: torch.Tensor, what: str, device, n=None, width=None) -> int:
@@ -857,10 +851,8 @@ def radamw_embedding_lookup(table: torch.Tensor, ids: torch.Tensor, out: torch.T
     n = ids.numel()
     idt = _index(ids, "ids", n, dev)
     os_ = _rows2d(out, "out", dev, n, dim)
-    with _scope(dev):
-        rc = lib.radamw_embedding_lookup(table.data_ptr(), _DTYPE_CODE[table.dtype], rows, dim, ts, ids.data_ptr(), idt,
-                                         n, float(scale), out.data_ptr(), _DTYPE_CODE[out.dtype], os_, _queue(dev))
-    _check(rc, "radamw_embedding_lookup")
+    _submit("radamw_embedding_lookup", lib.radamw_embedding_lookup, dev, table.data_ptr(), _DTYPE_CODE[table.dtype],
+            rows, dim, ts, ids.data_ptr(), idt, n, float(scale), out.data_ptr(), _DTYPE_CODE[out.dtype], os_)
 
 
 def radamw_embedding_grad_workspace_bytes(n: int, rows: int, dim: int) -> int:
@@ -885,12 +877,10 @@ def radamw_embedding_grad(grad_out: torch.Tensor, ids: torch.Tensor, table_grad:
     idt = _index(ids, "ids", n, dev)
     gs = _rows2d(grad_out, "grad_out", dev, n, dim)
     _dense(workspace, "workspace", device=dev)
-    with _scope(dev):
-        rc = lib.radamw_embedding_grad(grad_out.data_ptr(), _DTYPE_CODE[grad_out.dtype], gs, ids.data_ptr(), idt, n,
-                                       rows, dim, float(scale), -1 if padding_id is None else int(padding_id),
-                                       int(bool(accumulate)), table_grad.data_ptr(), _DTYPE_CODE[table_grad.dtype], ts,
-                                       workspace.data_ptr(), workspace.numel() * workspace.element_size(), _queue(dev))
-    _check(rc, "radamw_embedding_grad")
+    _submit("radamw_embedding_grad", lib.radamw_embedding_grad, dev, grad_out.data_ptr(), _DTYPE_CODE[grad_out.dtype],
+            gs, ids.data_ptr(), idt, n, rows, dim, float(scale), -1 if padding_id is None else int(padding_id),
+            int(bool(accumulate)), table_grad.data_ptr(), _DTYPE_CODE[table_grad.dtype], ts, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
 
 
 def radamw_policy_options_default() -> PolicyOptions:
@@ -935,11 +925,9 @@ def radamw_policy_loss(logits: torch.Tensor, labels: torch.Tensor, old_logp: Opt
     los = _row_values(loss, "loss", n, di)
     lgp = _row_values(logp, "logp", n, di)
     sta = _row_values(row_stats, "row_stats", 4 * n, di)
-    with _scope(dev):
-        rc = lib.radamw_policy_loss(logits.data_ptr(), _DTYPE_CODE[logits.dtype], n, vocab, st, labels.data_ptr(), idt,
-                                    old, ref, adv, wts, ctypes.byref(opts), float(grad_scale), tot, los, lgp, sta, gp,
-                                    gs, _queue(dev))
-    _check(rc, "radamw_policy_loss")
+    _submit("radamw_policy_loss", lib.radamw_policy_loss, dev, logits.data_ptr(), _DTYPE_CODE[logits.dtype], n, vocab,
+            st, labels.data_ptr(), idt, old, ref, adv, wts, ctypes.byref(opts), float(grad_scale), tot, los, lgp, sta,
+            gp, gs)
 
 
 def radamw_preference_loss(logits: torch.Tensor, labels: torch.Tensor, offsets: torch.Tensor, ref_logp: torch.Tensor,
@@ -964,11 +952,9 @@ def radamw_preference_loss(logits: torch.Tensor, labels: torch.Tensor, offsets: 
     seq = _row_values(seq_logp, "seq_logp", 2 * pairs, di)
     lgp = _row_values(logp, "logp", n, di)
     sta = _row_values(row_stats, "row_stats", 4 * n, di)
-    with _scope(dev):
-        rc = lib.radamw_preference_loss(logits.data_ptr(), _DTYPE_CODE[logits.dtype], n, vocab, st, labels.data_ptr(),
-                                        idt, offsets.data_ptr(), pairs, ref, wts, ctypes.byref(opts), float(grad_scale),
-                                        tot, los, seq, lgp, sta, gp, gs, _queue(dev))
-    _check(rc, "radamw_preference_loss")
+    _submit("radamw_preference_loss", lib.radamw_preference_loss, dev, logits.data_ptr(), _DTYPE_CODE[logits.dtype],
+            n, vocab, st, labels.data_ptr(), idt, offsets.data_ptr(), pairs, ref, wts, ctypes.byref(opts),
+            float(grad_scale), tot, los, seq, lgp, sta, gp, gs)
 
 
 def radamw_logits_grad(logits: torch.Tensor, labels: torch.Tensor, row_stats: torch.Tensor, grad: torch.Tensor,
@@ -981,10 +967,8 @@ def radamw_logits_grad(logits: torch.Tensor, labels: torch.Tensor, row_stats: to
     dev, n, vocab, st, idt, gp, gs = _logits(logits, labels, grad)
     sta = _row_values(row_stats, "row_stats", 4 * n, dev.index)
     ups = _row_values(upstream, "upstream", 1, dev.index)
-    with _scope(dev):
-        rc = lib.radamw_logits_grad(logits.data_ptr(), _DTYPE_CODE[logits.dtype], n, vocab, st, labels.data_ptr(), idt,
-                                    sta, ups, float(grad_scale), gp, gs, _queue(dev))
-    _check(rc, "radamw_logits_grad")
+    _submit("radamw_logits_grad", lib.radamw_logits_grad, dev, logits.data_ptr(), _DTYPE_CODE[logits.dtype], n, vocab,
+            st, labels.data_ptr(), idt, sta, ups, float(grad_scale), gp, gs)
 
 
 def radamw_host_coefficients(opts: Options, t: int, gradient_scale: float = 1.0) -> list[float]:
