@@ -156,22 +156,28 @@ __device__ __forceinline__ void clear_rows_of(const ClearArgs &a, int64_t block)
     const int mine = threadIdx.x >> a.lg, lane = threadIdx.x & 63;
     const int64_t begin = a.begin + block * a.rows_per_block;
     const int64_t end = begin + a.rows_per_block < a.end ? begin + a.rows_per_block : a.end;
-    const u32x4 z = {0, 0, 0, 0};
-    for (int64_t r0 = begin; r0 < end; r0 += 64) {
-        // the flags of 64 rows in one load
-        const int rows = static_cast<int>(end - r0 < 64 ? end - r0 : 64);
-        const uint64_t left = a.present ? __ballot(lane < rows && a.present[lane < rows ? r0 + lane : r0] != 0) : 0;
-        for (int r = mine; r < rows; r += per) {
-            if ((left >> r) & 1) continue;
-            char *dst = static_cast<char *>(a.table) + (r0 + r) * a.stride * elem_bytes<TDT>;
-            for (int64_t e = int64_t(threadIdx.x & (lanes - 1)) * E; e < a.dim; e += lanes * E) {
-                if (e + E <= a.dim) {
-                    stream_out<TDT>(dst, e, z);
-                } else {
-                    for (int64_t k = e; k < a.dim; ++k) store_value<TDT>(dst, k, 0.0f);
-                }
+    const auto clear = [&](int64_t r) {
+        const u32x4 z = {0, 0, 0, 0};
+        char *dst = static_cast<char *>(a.table) + r * a.stride * elem_bytes<TDT>;
+        for (int64_t e = int64_t(threadIdx.x & (lanes - 1)) * E; e < a.dim; e += lanes * E) {
+            if (e + E <= a.dim) {
+                stream_out<TDT>(dst, e, z);
+            } else {
+                for (int64_t k = e; k < a.dim; ++k) store_value<TDT>(dst, k, 0.0f);
             }
         }
+    };
+    if (!a.present || per >= 64) {
+        for (int64_t r = begin + mine; r < end; r += per)
+            if (!a.present || !a.present[r]) clear(r);
+        return;
+    }
+    for (int64_t r0 = begin; r0 < end; r0 += 64) {
+        // few rows at a time: the flags of 64 in one load
+        const int rows = static_cast<int>(end - r0 < 64 ? end - r0 : 64);
+        const uint64_t left = __ballot(lane < rows && a.present[lane < rows ? r0 + lane : r0] != 0);
+        for (int r = mine; r < rows; r += per)
+            if (!((left >> r) & 1)) clear(r0 + r);
     }
 }
 
@@ -308,6 +314,8 @@ template <int BLOCK, int ROUNDS>
 __global__ __launch_bounds__(BLOCK) void sort_small(SortKeys s, int bits, int passes, uint32_t *keys_out,
                                                                uint32_t *pos_out, ClearArgs clear) {
     constexpr int WAVES = BLOCK / 64;
+    constexpr int OWN = (1 << SORT_SMALL_BITS) > BLOCK ? (1 << SORT_SMALL_BITS) / BLOCK : 1;  // digits per thread
+    static_assert(OWN * BLOCK >= 1 << SORT_SMALL_BITS, "every digit has a thread");
     if (blockIdx.x > 0) {
         clear_rows<BLOCK>(clear, blockIdx.x - 1);
         return;
@@ -328,22 +336,27 @@ __global__ __launch_bounds__(BLOCK) void sort_small(SortKeys s, int bits, int pa
     Ranker<WAVES, ROUNDS> rk;
     for (int pass = 0; pass < passes; ++pass) {
         rk.count(key, rounds, first, s.n, pass * bits, bits, hist, bins);
-        // thread b: digit b's keys over the waves, then over the digits
-        uint32_t of[WAVES], mine = 0;
+        // thread t owns digits OWN t .. OWN t + OWN - 1: their keys over the
+        // waves, then over the digits
+        uint32_t of[OWN][WAVES], mine = 0;
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w) {
-            of[w] = tid < bins ? hist[w * bins + tid] : 0;
-            mine += of[w];
-        }
-        uint32_t all;
-        uint32_t at = block_scan<WAVES>(mine, part, &all);
-        if (tid < bins) {
+        for (int o = 0; o < OWN; ++o)
 #pragma unroll
             for (int w = 0; w < WAVES; ++w) {
-                hist[w * bins + tid] = at;
-                at += of[w];
+                of[o][w] = tid * OWN + o < bins ? hist[w * bins + tid * OWN + o] : 0;
+                mine += of[o][w];
             }
-        }
+        uint32_t all;
+        uint32_t at = block_scan<WAVES>(mine, part, &all);
+#pragma unroll
+        for (int o = 0; o < OWN; ++o)
+            if (tid * OWN + o < bins) {
+#pragma unroll
+                for (int w = 0; w < WAVES; ++w) {
+                    hist[w * bins + tid * OWN + o] = at;
+                    at += of[o][w];
+                }
+            }
         __syncthreads();
 #pragma unroll
         for (int r = 0; r < ROUNDS; ++r) {
@@ -462,6 +475,7 @@ __global__ __launch_bounds__(SORT_BLOCK) void radix_scatter(SortKeys s, int shif
         return;
     }
     constexpr int OWN = SORT_MAX_BINS / SORT_BLOCK;  // digits per thread
+    static_assert(OWN * SORT_BLOCK >= SORT_MAX_BINS, "every digit has a thread");
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
     const int bins = 1 << bits;
     const int64_t tile = blockIdx.x;

@@ -54,6 +54,21 @@ def test_lookup(dim, table_dtype, out_dtype):
     assert bool(whole[:, dim:].isnan().all())  # columns behind the row are left
 
 
+@pytest.mark.parametrize("n,dim", [(70_000, 40), (70_001, 33), (9000, 516), (5000, 2051), (5000, 4101), (3001, 8200)])
+@pytest.mark.parametrize("table_dtype,out_dtype", [(F32, BF16), (BF16, BF16), (F16, F32)])
+def test_lookup_long_lists(n, dim, table_dtype, out_dtype):
+    """Lists long enough for four pieces per lane."""
+    announce(f"lookup n={n} dim={dim}")
+    rows = 700
+    table = randn((rows, dim), dim, 1.0, table_dtype)
+    ids = randint(-1, rows, (n,), dim)
+    out = torch.full((n, dim), float("nan"), dtype=out_dtype, device=DEV)
+    ra.radamw_embedding_lookup(table.to(DEV), ids.to(DEV), out)
+    t = table.float().to(out_dtype).to(DEV)
+    want = torch.where((ids >= 0).to(DEV)[:, None], t[ids.clamp(min=0).to(DEV)], torch.zeros((), dtype=out_dtype, device=DEV))
+    assert torch.equal(out, want)
+
+
 @pytest.mark.parametrize("n", [0, 1, 2, 63, 4097])
 def test_lookup_lengths_and_ids_outside(n):
     announce(f"lookup n={n}")
@@ -149,6 +164,18 @@ def test_grad_lengths(n, rows):
     announce(f"grad n={n} rows={rows}")
     ids = randint(-2, rows + 2, (n,), n + rows)
     check_grad(n, rows, 16, F32, F32, ids, 0.5, None, False, n)
+
+
+@pytest.mark.parametrize("rows", [255, 256, 511, 512, 65_535, 65_536, 119_102, 262_143, 262_144])
+@pytest.mark.parametrize("n", [5, 254, 1024, 1025, 8200])
+def test_grad_digit_widths(rows, n):
+    """Digits of every width, up to 512 of them with four waves and with
+    sixteen, and 1024 in the tiled sort; ids from the whole range."""
+    announce(f"grad rows={rows} n={n}")
+    ids = torch.linspace(0, rows - 1, n).long()
+    ids = ids[torch.randperm(n, generator=torch.Generator().manual_seed(n))]
+    check_grad(n, rows, 8, F32, BF16, ids, 1.0, None, False, n)
+    check_grad(n, rows, 8, F32, BF16, ids.int(), 1.0, None, True, n)
 
 
 @pytest.mark.parametrize("rows", [600_000, 1_100_000])
