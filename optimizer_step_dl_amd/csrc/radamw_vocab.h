@@ -36,7 +36,7 @@ hipError_t launch_embedding_lookup(const LookupArgs &a, int tdt, int odt, hipStr
 constexpr int SORT_SMALL_MAX = 8192;
 constexpr int SORT_TINY_MAX = 1024;
 // Tokens of one tile of the tiled sort.
-constexpr int64_t SORT_TILE = 4096;
+constexpr int64_t SORT_TILE = 2048;
 constexpr int SORT_MAX_DIGIT_BITS = 10;
 
 // Workspace of an embedding gradient over n tokens (byte offsets).
