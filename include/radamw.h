@@ -614,9 +614,10 @@ int radamw_host_coefficients(const radamw_options *opts, uint64_t t, double grad
  *   - Like every entry point they refuse a stream under graph capture.
  *   - Calls keep nothing: two calls may run at once, on any streams, as long
  *     as they share no output and no workspace.
- *   - Limits (RADAMW_ERR_RANGE): dim <= 2^24, vocab <= 2^27, rows and n below
- *     2^31 and such that a launch needs at most 2^24 - 1 workgroups (n up to
- *     2^24 - 1 always fits for the losses and the lookup).
+ *   - Limits (RADAMW_ERR_RANGE): dim <= 2^24, vocab <= 2^27, rows and n up to
+ *     2^31 - 16, pairs below 2^24; a lookup or embedding gradient that needs
+ *     more than 2^24 - 1 workgroups (n below 2^24 always fits the lookup, n
+ *     below 2^30 with n * dim below 2^40 the gradient).
  */
 typedef enum {
     RADAMW_I32 = 0,
@@ -685,8 +686,8 @@ int radamw_embedding_grad(const void *grad_out, radamw_dtype grad_dtype, int64_t
  *   grad       : [n, vocab] of dtype, row stride grad_stride; NULL for the
  *                loss alone.  May be exactly the logits (same pointer and
  *                stride), which it then replaces.
- * Everything per row is formed in FP64 from the row's maximum and its sum of
- * exponentials (FP32 by lane, joined in FP64).  Where the gradient is asked
+ * Everything per row is formed in FP64 from the row's sum of exponentials
+ * (FP32 by lane, joined in FP64).  Where the gradient is asked
  * for, the logits of rows up to 256 KiB are read once.
  */
 typedef struct {
@@ -744,7 +745,9 @@ int radamw_preference_loss(const void *logits, radamw_dtype dtype, int64_t n, in
  * The logits' gradient of either loss from the records its forward call
  * left, for a backward pass that learns its scale only then:
  *   grad[i, j] = upstream * grad_scale * coef_i * (1[j = labels_i] - p_ij)
- *   row_stats : 4 n FP32 {max, 1 / sum of exponentials, coef, 1 - p_label}.
+ *   row_stats : 4 n FP32, per row {m, 1 / sum of exponentials relative to m,
+ *               coef, 1 - p_label}, m a logit near the largest; as written
+ *               by the forward call, whose dtype this one shares.
  *   upstream  : 1 FP32 on the device, or NULL: 1.
  * logits and labels are those of the forward call, unchanged.  grad may be
  * exactly the logits.

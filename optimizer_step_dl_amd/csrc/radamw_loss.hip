@@ -57,8 +57,9 @@ __device__ __forceinline__ double label_logp(float at_label, float shift, double
     return (double(at_label) * scale - double(shift)) * LN2 - log(sum);
 }
 
-// Sums below this have no exponential near FP32's largest value.
-constexpr double SUM_LIMIT = 0x1p100;
+// Sums below this have no exponential near FP32's largest value, and their
+// reciprocals times a coefficient none near its smallest.
+constexpr double SUM_LIMIT = 0x1p60;
 
 // Rows whose exponents are shifted by c = fl(m * LOG2E).
 __device__ __forceinline__ bool shiftable(float top) { return fabsf(top) < 16777216.0f; }
@@ -160,9 +161,10 @@ struct PolicyRow {
     // exponentials of a row are evaluated at once, in lanes 0, 1 and 2.
     __device__ __forceinline__ RowResult operator()(int64_t row, double logp) const {
         const int lane = threadIdx.x & 63;
-        const double old = old_logp ? double(old_logp[row]) : logp;
-        const double ref = kl_coef != 0.0 ? double(ref_logp[row]) : logp;
-        const double arg = lane == 0 ? logp - old : lane == 1 ? ref - logp : logp;
+        // without old_logp the ratio is 1, also where logp is -inf; a NaN stays one
+        const double moved = old_logp ? logp - double(old_logp[row]) : logp == logp ? 0.0 : logp;
+        const double away = kl_coef != 0.0 ? double(ref_logp[row]) - logp : 0.0;
+        const double arg = lane == 0 ? moved : lane == 1 ? away : logp;
         const double em1 = expm1(arg);
         const double r1 = __shfl(em1, 0, 64), k1 = __shfl(em1, 1, 64), p1 = __shfl(em1, 2, 64);
         const double ratio = r1 + 1.0, adv = advantages[row], w = weights ? double(weights[row]) : 1.0;
@@ -174,7 +176,7 @@ struct PolicyRow {
         const bool active = adv >= 0.0 ? !(ratio > hi) : !(ratio < lo);
         double d = active ? -plain : 0.0;
         if (kl_coef != 0.0) {
-            l += kl_coef * (k1 - (ref - logp));
+            l += kl_coef * (k1 - away);
             d -= kl_coef * k1;
         }
         if (lane == 0) loss[row] = static_cast<float>(l);
@@ -240,7 +242,8 @@ __device__ __forceinline__ RowResult finish_row(const ROW &f, const LogitsArgs &
                                     static_cast<float>(r.one_less_p)};
     } else {
         const float less = static_cast<float>(-expm1(logp));
-        if (lead) x.stats[row] = RowStats{top, static_cast<float>(1.0 / sum), static_cast<float>(logp - double(lp)), less};
+        const float rest = __builtin_isfinite(lp) ? static_cast<float>(logp - double(lp)) : 0.0f;
+        if (lead) x.stats[row] = RowStats{top, static_cast<float>(1.0 / sum), rest, less};
     }
     return r;
 }
@@ -334,7 +337,7 @@ template <int DT, int NT, int CH, bool GRAD, typename ROW>
 __global__ __launch_bounds__(NT) void loss_rows(LogitsArgs x, ROW f) {
     constexpr int E = chunk_elems<DT>;
     __shared__ RowShared<NT> sh;
-    const int64_t row = blockIdx.x;
+    const int64_t row = x.row0 + blockIdx.x;
     const int tid = threadIdx.x, wave = tid >> 6;
     char *out = static_cast<char *>(x.grad) + row * x.grad_stride * elem_bytes<DT>;
     int64_t label;
@@ -419,7 +422,7 @@ template <int DT, bool GRAD, typename ROW>
 __global__ __launch_bounds__(STREAM_BLOCK) void loss_rows_long(LogitsArgs x, ROW f) {
     constexpr int E = chunk_elems<DT>, NT = STREAM_BLOCK, U = STREAM_UNROLL;
     __shared__ RowShared<NT> sh;
-    const int64_t row = blockIdx.x;
+    const int64_t row = x.row0 + blockIdx.x;
     const int tid = threadIdx.x, wave = tid >> 6;
     char *out = static_cast<char *>(x.grad) + row * x.grad_stride * elem_bytes<DT>;
     int64_t label;
@@ -523,7 +526,7 @@ constexpr int GRAD_BLOCK = 1024;
 template <int DT>
 __global__ __launch_bounds__(GRAD_BLOCK) void logits_grad(LogitsArgs x, const float *upstream) {
     constexpr int E = chunk_elems<DT>;
-    const int64_t row = blockIdx.x;
+    const int64_t row = x.row0 + blockIdx.x;
     const int tid = threadIdx.x, at = static_cast<int>(blockIdx.y) * GRAD_BLOCK + tid;
     char *out = static_cast<char *>(x.grad) + row * x.grad_stride * elem_bytes<DT>;
     const char *in = static_cast<const char *>(x.logits) + row * x.stride * elem_bytes<DT>;
@@ -566,8 +569,10 @@ __global__ __launch_bounds__(GRAD_BLOCK) void logits_grad(LogitsArgs x, const fl
 constexpr int TOTAL_BLOCK = 1024;
 
 // total = sum of weights[i] * loss[i] in a fixed order; entries of weight
-// zero add nothing, whatever their loss.
+// zero add nothing, whatever their loss, nor do rows whose label is outside
+// 0 .. vocab - 1 (labels may be null), whatever their weight.
 __global__ __launch_bounds__(TOTAL_BLOCK) void weighted_total(const float *loss, const float *weights, int64_t n,
+                                                              const void *labels, int32_t wide, int64_t vocab,
                                                               float *total) {
     __shared__ double part[TOTAL_BLOCK / 64];
     double s = 0.0;
@@ -578,6 +583,10 @@ __global__ __launch_bounds__(TOTAL_BLOCK) void weighted_total(const float *loss,
             const int64_t i = i0 + u * TOTAL_BLOCK;
             l[u] = i < n ? loss[i] : 0.0f;
             w[u] = i >= n ? 0.0f : weights ? weights[i] : 1.0f;
+            if (labels && i < n) {
+                const int64_t a = load_index(labels, wide, i);
+                if (a < 0 || a >= vocab) w[u] = 0.0f;
+            }
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u)
@@ -623,7 +632,8 @@ __device__ __forceinline__ void pair_loss(const PreferenceArgs &a, int64_t pair,
     const double up = (h >= 0.0 ? 1.0 : q) / (1.0 + q), down = (h >= 0.0 ? q : 1.0) / (1.0 + q);  // sigmoid(h), sigmoid(-h)
     const double ls = a.label_smoothing, w = a.weights ? double(a.weights[pair]) : 1.0;
     const double plus = h > 0.0 ? 0.0 : -h, minus = h < 0.0 ? 0.0 : h;
-    *loss = static_cast<float>((1.0 - ls) * (plus + tail) + ls * (minus + tail));
+    // a term without weight adds nothing, infinite or not
+    *loss = static_cast<float>((ls < 1.0 ? (1.0 - ls) * (plus + tail) : 0.0) + (ls > 0.0 ? ls * (minus + tail) : 0.0));
     *coef = w == 0.0 ? 0.0f : static_cast<float>(w * a.beta * (ls * up - (1.0 - ls) * down));
 }
 
@@ -713,10 +723,27 @@ __global__ __launch_bounds__(FEW_BLOCK) void preference_few(PreferenceArgs a) {
 
 // ------------------------------------------------------------- launchers --
 
+// Rows of one launch: 2^21 workgroups of 1024 lanes stay below the 2^32
+// work-items that a launch addresses.
+constexpr int64_t ROWS_PER_LAUNCH = int64_t(1) << 21;
+
+// launch(x, rows) for all rows, in as many launches as that takes.
+template <typename LAUNCH>
+static hipError_t over_rows(LogitsArgs x, int *launched, LAUNCH launch) {
+    for (x.row0 = 0; x.row0 < x.n; x.row0 += ROWS_PER_LAUNCH) {
+        const int64_t rows = x.n - x.row0 < ROWS_PER_LAUNCH ? x.n - x.row0 : ROWS_PER_LAUNCH;
+        launch(x, static_cast<unsigned>(rows));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        ++*launched;
+    }
+    return hipSuccess;
+}
+
 template <int DT, bool GRAD, typename ROW>
-static hipError_t launch_rows(const LogitsArgs &x, const ROW &f, hipStream_t stream) {
+static void launch_rows(const LogitsArgs &x, unsigned rows, const ROW &f, hipStream_t stream) {
     const int64_t chunks = (x.vocab + chunk_elems<DT> - 1) / chunk_elems<DT>;
-    const dim3 grid(static_cast<unsigned>(x.n));
+    const dim3 grid(rows);
 #define RADAMW_ROWS(NT, CH) \
     hipLaunchKernelGGL((loss_rows<DT, NT, CH, GRAD, ROW>), grid, dim3(NT), 0, stream, x, f)
 #define RADAMW_LONG() \
@@ -737,49 +764,53 @@ static hipError_t launch_rows(const LogitsArgs &x, const ROW &f, hipStream_t str
     }
 #undef RADAMW_LONG
 #undef RADAMW_ROWS
-    return hipGetLastError();
 }
 
 template <int DT>
-static hipError_t policy_rows(const LogitsArgs &x, const PolicyRow &f, hipStream_t stream) {
-    return x.grad ? launch_rows<DT, true>(x, f, stream) : launch_rows<DT, false>(x, f, stream);
+static void policy_rows(const LogitsArgs &x, unsigned rows, const PolicyRow &f, hipStream_t stream) {
+    if (x.grad) launch_rows<DT, true>(x, rows, f, stream);
+    else launch_rows<DT, false>(x, rows, f, stream);
 }
 
 hipError_t launch_policy_loss(const PolicyArgs &a, int dt, hipStream_t stream, int *launched) {
     const PolicyRow f{a.old_logp, a.ref_logp, a.advantages, a.weights, a.loss, a.clip_low, a.clip_high, a.kl_coef};
-    hipError_t e = hipSuccess;
-    if (a.x.n > 0) {
-        e = dt == G_F32 ? policy_rows<G_F32>(a.x, f, stream)
-            : dt == G_F16 ? policy_rows<G_F16>(a.x, f, stream) : policy_rows<G_BF16>(a.x, f, stream);
-        if (e != hipSuccess) return e;
-        ++*launched;
-    }
-    hipLaunchKernelGGL(weighted_total, dim3(1), dim3(TOTAL_BLOCK), 0, stream, a.loss, a.weights, a.x.n, a.total);
+    hipError_t e = over_rows(a.x, launched, [&](const LogitsArgs &x, unsigned rows) {
+        switch (dt) {
+        case G_F32: policy_rows<G_F32>(x, rows, f, stream); break;
+        case G_F16: policy_rows<G_F16>(x, rows, f, stream); break;
+        default: policy_rows<G_BF16>(x, rows, f, stream); break;
+        }
+    });
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(weighted_total, dim3(1), dim3(TOTAL_BLOCK), 0, stream, a.loss, a.weights, a.x.n,
+                       a.x.labels, a.x.wide_ids, a.x.vocab, a.total);
     if ((e = hipGetLastError()) == hipSuccess) ++*launched;
     return e;
 }
 
-hipError_t launch_logits_grad(const LogitsArgs &x, const float *upstream, int dt, hipStream_t stream) {
-    const int64_t chunks = (x.vocab + (dt == G_F32 ? 3 : 7)) / (dt == G_F32 ? 4 : 8);
-    const dim3 grid(static_cast<unsigned>(x.n), static_cast<unsigned>((chunks + GRAD_BLOCK - 1) / GRAD_BLOCK));
-    const dim3 block(GRAD_BLOCK);
-    switch (dt) {
-    case G_F32: hipLaunchKernelGGL(logits_grad<G_F32>, grid, block, 0, stream, x, upstream); break;
-    case G_F16: hipLaunchKernelGGL(logits_grad<G_F16>, grid, block, 0, stream, x, upstream); break;
-    default: hipLaunchKernelGGL(logits_grad<G_BF16>, grid, block, 0, stream, x, upstream); break;
-    }
-    return hipGetLastError();
+hipError_t launch_logits_grad(const LogitsArgs &a, const float *upstream, int dt, hipStream_t stream, int *launched) {
+    const int64_t chunks = (a.vocab + (dt == G_F32 ? 3 : 7)) / (dt == G_F32 ? 4 : 8);
+    const unsigned parts = static_cast<unsigned>((chunks + GRAD_BLOCK - 1) / GRAD_BLOCK);
+    return over_rows(a, launched, [&](const LogitsArgs &x, unsigned rows) {
+        const dim3 grid(rows, parts), block(GRAD_BLOCK);
+        switch (dt) {
+        case G_F32: hipLaunchKernelGGL(logits_grad<G_F32>, grid, block, 0, stream, x, upstream); break;
+        case G_F16: hipLaunchKernelGGL(logits_grad<G_F16>, grid, block, 0, stream, x, upstream); break;
+        default: hipLaunchKernelGGL(logits_grad<G_BF16>, grid, block, 0, stream, x, upstream); break;
+        }
+    });
 }
 
 hipError_t launch_preference_loss(const PreferenceArgs &a, int dt, hipStream_t stream, int *launched) {
     const LogpRow f{};
-    hipError_t e = hipSuccess;
-    if (a.x.n > 0) {
-        e = dt == G_F32 ? launch_rows<G_F32, false>(a.x, f, stream)
-            : dt == G_F16 ? launch_rows<G_F16, false>(a.x, f, stream) : launch_rows<G_BF16, false>(a.x, f, stream);
-        if (e != hipSuccess) return e;
-        ++*launched;
-    }
+    hipError_t e = over_rows(a.x, launched, [&](const LogitsArgs &x, unsigned rows) {
+        switch (dt) {
+        case G_F32: launch_rows<G_F32, false>(x, rows, f, stream); break;
+        case G_F16: launch_rows<G_F16, false>(x, rows, f, stream); break;
+        default: launch_rows<G_BF16, false>(x, rows, f, stream); break;
+        }
+    });
+    if (e != hipSuccess) return e;
     if (a.pairs <= FEW_PAIRS) {
         hipLaunchKernelGGL(preference_few, dim3(1), dim3(FEW_BLOCK), 0, stream, a);
         if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -787,14 +818,12 @@ hipError_t launch_preference_loss(const PreferenceArgs &a, int dt, hipStream_t s
     } else {
         hipLaunchKernelGGL(preference_pairs, dim3(static_cast<unsigned>(a.pairs)), dim3(PAIR_BLOCK), 0, stream, a);
         if ((e = hipGetLastError()) != hipSuccess) return e;
-        hipLaunchKernelGGL(weighted_total, dim3(1), dim3(TOTAL_BLOCK), 0, stream, a.loss, a.weights, a.pairs, a.total);
+        hipLaunchKernelGGL(weighted_total, dim3(1), dim3(TOTAL_BLOCK), 0, stream, a.loss, a.weights, a.pairs,
+                           nullptr, 0, 0, a.total);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         *launched += 2;
     }
-    if (a.x.grad && a.x.n > 0) {
-        if ((e = launch_logits_grad(a.x, nullptr, dt, stream)) != hipSuccess) return e;
-        ++*launched;
-    }
+    if (a.x.grad) e = launch_logits_grad(a.x, nullptr, dt, stream, launched);
     return e;
 }
 

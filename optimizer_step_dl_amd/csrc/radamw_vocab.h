@@ -91,6 +91,7 @@ struct LogitsArgs {
     int32_t wide_ids;
     RowStats *stats;           // may be null for a policy loss
     float *logp;
+    int64_t row0;              // first row of a launch
 };
 
 struct PolicyArgs {
@@ -112,6 +113,6 @@ struct PreferenceArgs {
 hipError_t launch_preference_loss(const PreferenceArgs &a, int dt, hipStream_t stream, int *launched);
 
 // grad = upstream * grad_scale * coef * (1[label] - p) from saved records.
-hipError_t launch_logits_grad(const LogitsArgs &a, const float *upstream, int dt, hipStream_t stream);
+hipError_t launch_logits_grad(const LogitsArgs &a, const float *upstream, int dt, hipStream_t stream, int *launched);
 
 }  // namespace radamw

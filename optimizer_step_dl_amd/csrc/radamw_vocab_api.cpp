@@ -105,7 +105,7 @@ int check_logits_shape(int64_t n, int64_t vocab, int64_t stride, const void *gra
     int rc;
     if ((rc = check_rows(n, vocab, stride, MAX_VOCAB))) return rc;
     if (grad && (rc = check_rows(n, vocab, grad_stride, MAX_VOCAB))) return rc;
-    return n > LAUNCH_MAX_BLOCKS ? RADAMW_ERR_RANGE : RADAMW_OK;
+    return RADAMW_OK;
 }
 
 }  // namespace
@@ -203,7 +203,7 @@ int radamw_policy_loss(const void *logits, radamw_dtype dtype, int64_t n, int64_
     DeviceScope scope(dev);
     Buffers b(dev);
     LogitsArgs x{logits, labels, n, vocab, stride, grad, grad_stride, static_cast<float>(grad_scale),
-                 labels_type == RADAMW_I64, reinterpret_cast<RowStats *>(row_stats), logp};
+                 labels_type == RADAMW_I64, reinterpret_cast<RowStats *>(row_stats), logp, 0};
     const bool kl = opts->kl_coef != 0.0;
     if ((rc = check_logits(x, dtype, labels_type, b))) return rc;
     if (old_logp && (rc = b.add(old_logp, 4, n * 4, false))) return rc;
@@ -245,7 +245,7 @@ int radamw_preference_loss(const void *logits, radamw_dtype dtype, int64_t n, in
     DeviceScope scope(dev);
     Buffers b(dev);
     LogitsArgs x{logits, labels, n, vocab, stride, grad, grad_stride, static_cast<float>(grad_scale),
-                 index_type == RADAMW_I64, reinterpret_cast<RowStats *>(row_stats), logp};
+                 index_type == RADAMW_I64, reinterpret_cast<RowStats *>(row_stats), logp, 0};
     if ((rc = check_logits(x, dtype, index_type, b))) return rc;
     const int64_t is = static_cast<int64_t>(index_bytes(index_type));
     if ((rc = b.add(offsets, index_bytes(index_type), (2 * pairs + 1) * is, false))) return rc;
@@ -280,14 +280,15 @@ int radamw_logits_grad(const void *logits, radamw_dtype dtype, int64_t n, int64_
     DeviceScope scope(dev);
     Buffers b(dev);
     LogitsArgs x{logits, labels, n, vocab, stride, grad, grad_stride, static_cast<float>(grad_scale),
-                 labels_type == RADAMW_I64, reinterpret_cast<RowStats *>(const_cast<float *>(row_stats)), nullptr};
+                 labels_type == RADAMW_I64, reinterpret_cast<RowStats *>(const_cast<float *>(row_stats)), nullptr, 0};
     if ((rc = check_logits(x, dtype, labels_type, b))) return rc;
     if ((rc = b.add(row_stats, 16, n * 16, false))) return rc;
     if (upstream && (rc = b.add(upstream, 4, 4, false))) return rc;
     if ((rc = b.alias())) return rc;
-    if ((rc = hip_status(launch_logits_grad(x, upstream, dtype, stream)))) return rc;
-    count_launches(1);
-    return RADAMW_OK;
+    int launched = 0;
+    rc = hip_status(launch_logits_grad(x, upstream, dtype, stream, &launched));
+    count_launches(launched);
+    return rc;
 }
 
 }  // extern "C"

@@ -57,7 +57,8 @@ class _Embedding(torch.autograd.Function):
         ctx.save_for_backward(ids)
         ctx.scale, ctx.padding_id, ctx.grad_buffer = scale, padding_id, grad_buffer
         ctx.shape = (rows, dim)
-        ctx.grad_dtype = getattr(table, "grad_dtype", None) or table.dtype
+        # the dtype a leaf keeps its gradient in, where this torch knows one
+        ctx.grad_dtype = (getattr(table, "grad_dtype", None) if table.is_leaf else None) or table.dtype
         return out.view(*ids.shape, dim)
 
     @staticmethod
@@ -82,7 +83,7 @@ def embedding(ids: torch.Tensor, table: torch.Tensor, *, scale: float = 1.0, pad
 
     ``table`` [rows, dim] takes the gradient: the sum over tokens in a fixed
     order, tokens of ``padding_id`` left out, in ``table.grad_dtype`` where
-    that is set, else the table's dtype.  ``model_copy`` is a float16 /
+    a leaf has that set, else the table's dtype.  ``model_copy`` is a float16 /
     bfloat16 tensor of the same shape to read instead of the table (the copy
     FusedAdamW rewrites at every step).  ``out_dtype`` defaults to what is
     read.  With ``grad_buffer`` (a [rows, dim] tensor, as ``table.grad`` of a

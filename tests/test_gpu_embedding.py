@@ -215,6 +215,19 @@ def test_grad_uneven_ids(kind, n):
     check_grad(n, rows, dim, BF16, BF16, ids, 1.0, pad, True, n)
 
 
+@pytest.mark.parametrize("n", [8000, 16_000, 30_000])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_grad_chunk_lengths(n, accumulate):
+    """Lists long enough for chunks of 16, 32 and 64 tokens, runs that end at
+    every place of a chunk, one that crosses dozens."""
+    announce(f"grad chunks n={n}")
+    rows, dim = 900, 4100
+    ids = randint(0, rows, (n,), n)
+    ids[n // 4:n // 2] = 17
+    ids[-200:] = rows - 1
+    check_grad(n, rows, dim, BF16, BF16, ids, 1.0, 0, accumulate, n)
+
+
 def test_grad_sums_in_token_order():
     """Equal ids keep their tokens' order: values whose FP32 sum depends on
     it give the sum taken in order (one chunk of eight tokens)."""

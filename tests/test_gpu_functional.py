@@ -63,6 +63,20 @@ def test_embedding_grad_buffer_and_copy():
     assert torch.equal(buffer.float().cpu(), want)  # small whole numbers: exact
 
 
+def test_embedding_of_a_computed_table():
+    """A table that is itself a result (a tied, scaled or cast one)."""
+    announce("functional computed table")
+    leaf = torch.randn((9, 5), generator=gen(1)).to(DEV).requires_grad_()
+    ids = torch.tensor([3, 3, 8], device=DEV)
+    embedding(ids, leaf * 2).sum().backward()
+    want = torch.zeros(9, 5)
+    want[3], want[8] = 4, 2
+    assert torch.equal(leaf.grad.cpu(), want)
+    leaf.grad = None
+    embedding(ids, leaf.to(BF16)).sum().backward()
+    assert leaf.grad.dtype == F32 and torch.equal(leaf.grad.cpu(), want / 2)
+
+
 def test_embedding_16_bit_gradient_of_a_master():
     announce("functional embedding grad_dtype")
     table = torch.zeros((8, 4), device=DEV, requires_grad=True)

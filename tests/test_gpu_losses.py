@@ -242,13 +242,50 @@ def test_policy_absent_rows_may_hold_anything(vocab):
     taken[[2, 5]] = False
     clean = torch.where(taken, w, torch.zeros(()))
     opts = ra.policy_options(0.2, 0.28, 0.1)
-    o, g, *_ = run_policy(x, labels, old, adv, opts, ref, torch.where(taken, w, w.nan_to_num(0.3)))
+    o, g, *_ = run_policy(x, labels, old, adv, opts, ref, w)
     assert bool((g[[2, 5, 6]] == 0).all()) and bool((o["loss"][[2, 5, 6]] == 0).all())
     assert bool(o["total"].isfinite()) and bool(g.isfinite().all())
     check_policy(torch.where((taken & (w != 0))[:, None], x, torch.zeros((), dtype=BF16)), labels, taken,
                  old.nan_to_num(0), adv.nan_to_num(0), opts, ref.nan_to_num(0, 0), clean)
     o, g, *_ = run_policy(x, torch.full_like(labels, -1), old, adv, opts, ref, None)
     assert float(o["total"]) == 0.0 and bool((g == 0).all()) and bool((o["logp"] == 0).all())
+
+
+@pytest.mark.parametrize("vocab", [60, 20_000, 140_000])
+def test_impossible_labels(vocab):
+    """Labels whose own logit is -inf: their probability is 0, the ratio with
+    itself 1, a rejected sequence with one is infinitely far away."""
+    announce(f"impossible labels {vocab}")
+    x, labels, taken = make_rows(6, vocab, F32, 71, share=1.0)
+    for i in (1, 4):
+        x[i, labels[i]] = float("-inf")
+    adv = torch.tensor([1.0, -2.0, 0.5, 1.0, 1.0, 1.0])
+    o, g, *_ = run_policy(x, labels, None, adv, ra.policy_options())
+    assert bool(o["logp"][[1, 4]].isneginf().all()) and torch.equal(o["loss"].cpu(), -adv)
+    assert bool(g.isfinite().all()) and float(g[1, labels[1]]) == 2.0 and float(g[4, labels[4]]) == -1.0
+    old = torch.full((6,), -3.0)
+    o, g, *_ = run_policy(x, labels, old, adv.abs(), ra.policy_options())
+    assert bool((o["loss"][[1, 4]] == 0).all()) and bool((g[[1, 4]] == 0).all())
+    # chosen 0..3, rejected 3..6, which holds row 4
+    o, g, *_ = run_preference(x[[0, 2, 3, 5, 4, 1]], labels[[0, 2, 3, 5, 4, 1]], [0, 3, 5], torch.zeros(2),
+                              ra.preference_options())
+    assert o["seq_logp"].isneginf().tolist() == [False, True] and float(o["loss"]) == 0.0 and bool((g == 0).all())
+    o, g, *_ = run_preference(x[[4, 0, 2]], labels[[4, 0, 2]], [0, 1, 3], torch.zeros(2), ra.preference_options())
+    assert float(o["loss"]) == float("inf") and bool(g.isfinite().all())
+    assert abs(float(g[0, labels[4]]) + 0.1) < 1e-6
+
+
+def test_more_rows_than_a_launch_holds():
+    """2^21 rows and some: every kernel goes on with the next launch."""
+    announce("rows over launches")
+    n, vocab = (1 << 21) + 5, 8
+    x, labels, taken = make_rows(n, vocab, F32, 81)
+    taken[-3:] = True
+    labels[-3:] = torch.tensor([7, 0, 3])
+    adv = torch.randn(n, generator=gen(82))
+    check_policy(x, labels, taken, None, adv, ra.policy_options(), None, torch.full((n,), 1.0 / n))
+    bounds = [1, 1 << 20, (1 << 20) + 7, (1 << 21) - 1, n - 1]
+    check_preference(x, labels, taken, bounds, torch.zeros(4), ra.preference_options(1e-6, 0.1))
 
 
 def test_policy_gradient_against_differences():

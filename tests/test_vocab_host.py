@@ -93,7 +93,7 @@ def test_loss_refusals(lib):
         for kw in (dict(dt=3), dict(idt=2), dict(n=-1), dict(vocab=0), dict(st=7), dict(gs=7),
                    dict(scale=float("nan")), dict(scale=-1e40)):
             assert call(lib, opts, **kw) == INVALID, kw
-        for kw in (dict(n=2 ** 24), dict(vocab=2 ** 27 + 1, st=2 ** 27 + 1, gs=2 ** 27 + 1), dict(st=2 ** 47, n=1000)):
+        for kw in (dict(n=2 ** 31), dict(vocab=2 ** 27 + 1, st=2 ** 27 + 1, gs=2 ** 27 + 1), dict(st=2 ** 47, n=1000)):
             assert call(lib, opts, **kw) == RANGE, kw
     assert preference_call(lib, (0.1, 0.0), pairs=0) == INVALID
     assert preference_call(lib, (0.1, 0.0), pairs=2 ** 24) == RANGE
