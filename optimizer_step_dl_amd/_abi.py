@@ -795,6 +795,13 @@ def _submit(where: str, entry, device: torch.device, *args) -> None:
 def _rows2d(t: torch.Tensor, what: str, device, n=None, width=None) -> int:
     """Check a [n, width] device tensor with unit column stride; its row
     stride in elements."""
+    try:  # the usual case in few questions; what fails it is named below
+        (rows, cols), (row, col) = t.shape, t.stride()
+        if (col == 1 and rows > 1 and row >= cols and t.get_device() == device.index and t.dtype in _DTYPE_CODE
+                and (n is None or rows == n) and (width is None or cols == width)):
+            return row
+    except (AttributeError, TypeError, ValueError):
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{what} must be a device tensor")
     if t.device != device:
@@ -816,6 +823,9 @@ def _rows2d(t: torch.Tensor, what: str, device, n=None, width=None) -> int:
 
 def _index(t: torch.Tensor, what: str, n: int, device) -> int:
     """Check a contiguous index tensor of n entries; its type code."""
+    code = _INDEX_CODE.get(getattr(t, "dtype", None))
+    if code is not None and t.numel() == n and t.get_device() == device.index and t.is_contiguous():
+        return code
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{what} must be a device tensor")
     if t.dtype not in _INDEX_CODE:
