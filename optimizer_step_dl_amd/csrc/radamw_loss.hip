@@ -199,13 +199,14 @@ struct IsPolicy<PolicyRow> {
 
 template <typename ROW>
 __device__ __forceinline__ bool takes_part(const ROW &f, const LogitsArgs &x, int64_t row, int64_t *label) {
+    // both loads leave before either is looked at
     const int64_t a = load_index(x.labels, x.wide_ids, row);
-    *label = a;
-    bool in = a >= 0 && a < x.vocab;
+    float w = 1.0f;
     if constexpr (IsPolicy<ROW>::value) {
-        if (in && f.weights) in = !(f.weights[row] == 0.0f);
+        if (f.weights) w = f.weights[row];
     }
-    return in;
+    *label = a;
+    return a >= 0 && a < x.vocab && w != 0.0f;
 }
 
 template <typename ROW>
