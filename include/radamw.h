@@ -643,8 +643,8 @@ int radamw_embedding_lookup(const void *table, radamw_dtype table_dtype, int64_t
  * Gradient of the lookup with respect to the table:
  *   table_grad[v, :] = (accumulate ? table_grad[v, :] : 0)
  *                      + scale * sum of grad_out[t, :] over ids[t] == v
- * The token positions are sorted by id (stably) and each id's rows are
- * summed in FP32 in a fixed order; the result is rounded once.  Tokens whose
+ * Each id's rows are summed in FP32 in an order that the arguments fix, so
+ * that equal calls give equal bits; the result is rounded once.  Tokens whose
  * id is padding_id (-1: none) or outside 0 .. rows-1 add nothing.
  *   accumulate = 0 : all rows of table_grad are written (zeros where no token
  *                    adds).  Columns between dim and table_stride are left.

@@ -228,6 +228,50 @@ def test_grad_chunk_lengths(n, accumulate):
     check_grad(n, rows, dim, BF16, BF16, ids, 1.0, 0, accumulate, n)
 
 
+@pytest.mark.parametrize("kind", ["one id", "pairs", "heavy", "each once", "all outside"])
+@pytest.mark.parametrize("n", [1, 9, 64, 65, 255, 256, 257, 511, 512, 513])
+def test_grad_few(kind, n):
+    """Up to 512 tokens are summed without a sort: lists on both sides of a
+    wave's and a workgroup's tokens, ids with one token, two, more than eight
+    and all."""
+    announce(f"grad few {kind} n={n}")
+    rows, dim, pad = 1000, 1032, 3
+    if kind == "one id":
+        ids = torch.full((n,), 7)
+    elif kind == "pairs":  # a token and the one half a list behind it
+        ids = (torch.arange(n) % max(1, n // 2)) + 5
+    elif kind == "heavy":
+        ids = randint(-3, rows + 3, (n,), n)
+        ids[torch.rand(n, generator=torch.Generator().manual_seed(n)) < 0.4] = 400
+    elif kind == "each once":
+        ids = torch.randperm(rows, generator=torch.Generator().manual_seed(n))[:n]
+    else:
+        ids, pad = torch.full((n,), rows), 0
+    check_grad(n, rows, dim, BF16, F32, ids, 0.5, pad, False, n)
+    check_grad(n, rows, dim, F32, BF16, ids.int(), 0.5, pad, True, n)
+
+
+@pytest.mark.parametrize("dim", [4096, 4104])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_grad_few_widest(dim, accumulate):
+    """512 tokens at the widest rows summed without a sort, and one more
+    column tile."""
+    announce(f"grad few dim={dim}")
+    n, rows = 512, 700
+    check_grad(n, rows, dim, F16, F16, randint(0, rows // 4, (n,), dim), 1.0, None, accumulate, dim)
+
+
+@pytest.mark.parametrize("rows,dim", [(1, 3), (20_000, 1), (4_500_000, 2), (9000, 33), (3, 70_000)])
+def test_grad_few_clears(rows, dim):
+    """The rows without a token among few tokens: many rows to a workgroup,
+    the largest number of rows to one, and rows longer than its share."""
+    announce(f"grad few rows={rows} dim={dim}")
+    n = 20
+    ids = torch.linspace(0, rows - 1, n).long()
+    check_grad(n, rows, dim, F32, BF16, ids, 1.0, None, False, dim)
+    check_grad(0, rows, dim, F32, F32, ids[:0], 1.0, None, False, dim)
+
+
 def test_grad_sums_in_token_order():
     """Equal ids keep their tokens' order: values whose FP32 sum depends on
     it give the sum taken in order (one chunk of eight tokens)."""
