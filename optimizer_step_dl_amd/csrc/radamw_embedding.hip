@@ -12,7 +12,8 @@
 // 64 x 8 columns.  A run of equal ids inside one chunk is finished there; a
 // run that crosses chunks leaves FP32 partial sums, which a second launch
 // joins in the order of the chunks.  Equal chunks keep the waves balanced
-// however uneven the ids are.
+// however uneven the ids are.  A list of up to 512 tokens needs no sort: each
+// token's workgroup finds its equals among all ids.
 //
 // The sort is a few microseconds' latency of few workgroups, so the rows
 // that no token names are cleared by the other workgroups of its launches.
@@ -72,17 +73,18 @@ __global__ __launch_bounds__(ROW_BLOCK) void embedding_lookup(LookupArgs a, int 
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
         const int64_t e = (first + u * lanes) * 8;
-        if (inside && e + 8 <= a.dim) r[u] = load_raw8<TDT>(src, e);
+        if (inside && e < a.dim && a.dim >= 8) r[u] = load_raw8<TDT>(src, first_of_eight(e, a.dim));
     }
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
         const int64_t e = (first + u * lanes) * 8;
-        if (e + 8 <= a.dim) {
+        if (e >= a.dim) continue;
+        if (a.dim >= 8) {
             f32x8 v;
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = inside ? scaled(raw_value<TDT>(r[u], j), a.scale) : 0.0f;
-            stream8<ODT>(dst, e, v);
-        } else if (e < a.dim) {
+            stream8<ODT>(dst, first_of_eight(e, a.dim), v);
+        } else {
             for (int64_t k = e; k < a.dim; ++k)
                 store_value<ODT>(dst, k, inside ? scaled(load_value<TDT>(src, k), a.scale) : 0.0f);
         }
@@ -169,8 +171,8 @@ __device__ __forceinline__ void clear_rows_of(const ClearArgs &a, int64_t block)
         const u32x4 z = {0, 0, 0, 0};
         char *dst = static_cast<char *>(a.table) + r * a.stride * elem_bytes<TDT>;
         for (int64_t e = int64_t(threadIdx.x & (lanes - 1)) * E; e < a.dim; e += lanes * E) {
-            if (e + E <= a.dim) {
-                stream_out<TDT>(dst, e, z);
+            if (a.dim >= E) {
+                stream_out<TDT>(dst, e + E <= a.dim ? e : a.dim - E, z);
             } else {
                 for (int64_t k = e; k < a.dim; ++k) store_value<TDT>(dst, k, 0.0f);
             }
@@ -566,25 +568,35 @@ struct SumArgs {
     float scale;
 };
 
-// v into columns [e, e + 8) of table row `key`, rounded once.
+// v into the eight columns that the lane of columns e ... serves (from
+// first_of_eight on) of table row `key`, rounded once.  A column that two
+// lanes serve gets the same value from both; where that adds to the table,
+// the second keeps it to itself.
 template <int TDT, bool ACC>
 __device__ __forceinline__ void write_row(const SumArgs &a, uint32_t key, int64_t e, f32x8 v) {
     char *dst = static_cast<char *>(a.table_grad) + int64_t(key) * a.table_stride * elem_bytes<TDT>;
-    if (e + 8 <= a.dim) {
+    if (a.dim >= 8) {
+        const int64_t from = first_of_eight(e, a.dim);
         if constexpr (ACC) {
-            const Raw8<TDT> old = load_raw8<TDT>(dst, e);
+            const Raw8<TDT> old = load_raw8<TDT>(dst, from);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = __builtin_fmaf(v[j], a.scale, raw_value<TDT>(old, j));
+            if (from != e) {
+#pragma unroll
+                for (int j = 1; j < 8; ++j)
+                    if (from + j >= e) store_value<TDT>(dst, from + j, v[j]);
+                return;
+            }
         } else {
             v *= a.scale;
         }
-        store8<TDT>(dst, e, v);
+        store8<TDT>(dst, from, v);
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (e + j < a.dim) {
-                const float x = ACC ? __builtin_fmaf(v[j], a.scale, load_value<TDT>(dst, e + j)) : v[j] * a.scale;
-                store_value<TDT>(dst, e + j, x);
+        for (int j = 0; j < 7; ++j) {
+            if (j < a.dim) {
+                const float x = ACC ? __builtin_fmaf(v[j], a.scale, load_value<TDT>(dst, j)) : v[j] * a.scale;
+                store_value<TDT>(dst, j, x);
             }
         }
     }
@@ -592,22 +604,22 @@ __device__ __forceinline__ void write_row(const SumArgs &a, uint32_t key, int64_
 
 constexpr int SUM_UNROLL = 8;  // rows in flight per lane
 
-// Values e .. dim - 1 (fewer than eight) of a row, zeros behind.
+// The `dim` values (fewer than eight) of a row, zeros behind.
 template <int DT>
-__device__ __forceinline__ Raw8<DT> load_edge8(const void *p, int64_t e, int64_t dim) {
+__device__ __forceinline__ Raw8<DT> load_narrow8(const void *p, int64_t dim) {
     Raw8<DT> r;
 #pragma unroll
     for (int c = 0; c < (DT == G_F32 ? 2 : 1); ++c) r.c[c] = u32x4{0, 0, 0, 0};
 #pragma unroll
     for (int k = 0; k < 7; ++k) {
-        const uint32_t b = e + k < dim ? load_bits<DT>(p, e + k) : 0;
+        const uint32_t b = k < dim ? load_bits<DT>(p, k) : 0;
         if constexpr (DT == G_F32) r.c[k >> 2][k & 3] = b;
         else r.c[0][k >> 1] |= k & 1 ? b << 16 : b;
     }
     return r;
 }
 
-// Columns [e, e + 8) of one chunk of the sorted tokens.  The keys and
+// The lane's eight columns of one chunk of the sorted tokens.  The keys and
 // positions of a group of SUM_UNROLL tokens come in two wide loads (scalar
 // ones where a wave shares its chunk); entries behind the last token are read
 // and not used, and a token that takes no part reads row 0 in its place, so
@@ -619,7 +631,8 @@ __device__ __forceinline__ void sum_chunk(const SumArgs &a, int64_t chunk, int64
     const uint32_t *keys = a.keys + base, *pos = a.pos + base;
     const uint32_t rows = static_cast<uint32_t>(a.rows);
     if (keys[0] >= rows) return;  // sorted behind every id that takes part
-    const bool whole = e + 8 <= a.dim;
+    const bool whole = a.dim >= 8;
+    const int64_t from = first_of_eight(e, a.dim);
     bool continued = base > 0 && a.keys[base - 1] == keys[0];  // the first run began in an earlier chunk
     const bool more = base + count < a.n && a.keys[base + count] == keys[count - 1];
     f32x8 acc = 0.0f;
@@ -638,10 +651,10 @@ __device__ __forceinline__ void sum_chunk(const SumArgs &a, int64_t chunk, int64
         };
         if (whole) {
 #pragma unroll
-            for (int u = 0; u < SUM_UNROLL; ++u) raw[u] = stream_raw8<GDT>(source(u), e);
+            for (int u = 0; u < SUM_UNROLL; ++u) raw[u] = stream_raw8<GDT>(source(u), from);
         } else {
 #pragma unroll
-            for (int u = 0; u < SUM_UNROLL; ++u) raw[u] = load_edge8<GDT>(source(u), e, a.dim);
+            for (int u = 0; u < SUM_UNROLL; ++u) raw[u] = load_narrow8<GDT>(source(u), a.dim);
         }
 #pragma unroll
         for (int u = 0; u < SUM_UNROLL; ++u) {
@@ -655,11 +668,11 @@ __device__ __forceinline__ void sum_chunk(const SumArgs &a, int64_t chunk, int64
                 } else {
                     float *slot = a.partials + (2 * chunk + (continued ? 0 : 1)) * a.dim;
                     if (whole) {
-                        store8<G_F32>(slot, e, acc);
+                        store8<G_F32>(slot, from, acc);
                     } else {
 #pragma unroll
                         for (int k = 0; k < 7; ++k)
-                            if (e + k < a.dim) slot[e + k] = acc[k];
+                            if (k < a.dim) slot[k] = acc[k];
                     }
                 }
                 continued = false;
@@ -685,28 +698,35 @@ __global__ __launch_bounds__(ROW_BLOCK) void embedding_sum(SumArgs a, int lg) {
 }
 
 // Eight waves share a long run: 32705 tokens of FP32, 495 columns, whose most
-// frequent id is in 4% of them, join in 10.5 us, against 15 us with four (and
-// 10.2 with sixteen, which costs short lists 1 us).
+// frequent id is in 4% of them, join in 5.8 us, against 7.1 us with four and
+// 6.7 with sixteen; 30000 BF16 tokens of one id, 2048 columns, take 87 us in
+// all, against 119 and 98.
 constexpr int JOIN_BLOCK = 512;
 constexpr int JOIN_WAVES = JOIN_BLOCK / 64;
 constexpr int JOIN_UNROLL = 4;
 // Partial sums up to which one wave joins a run by itself.
 constexpr int64_t JOIN_ALONE = 16;
 
-// Partial sum i of the run that begins in chunk c, columns [e, e + 8).
-__device__ __forceinline__ Raw8<G_F32> load_partial8(const SumArgs &a, int64_t c, int64_t i, int64_t e) {
-    const float *slot = a.partials + (i == 0 ? 2 * c + 1 : 2 * (c + i)) * a.dim;
-    return e + 8 <= a.dim ? load_raw8<G_F32>(slot, e) : load_edge8<G_F32>(slot, e, a.dim);
-}
-
-// Sum of partial sums first, first + step, ... up to `last`, in that order.
+// Sum of the partial sums first, first + step, ... up to `last` of the run
+// that begins in chunk c, the lane's eight columns, in that order.
 __device__ __forceinline__ f32x8 sum_partials(const SumArgs &a, int64_t c, int64_t first, int64_t step, int64_t last,
                                               int64_t e) {
     f32x8 acc = 0.0f;
+    const bool whole = a.dim >= 8;
+    const int64_t from = first_of_eight(e, a.dim);
     for (int64_t i = first; i <= last; i += step * JOIN_UNROLL) {
         Raw8<G_F32> r[JOIN_UNROLL];
+        const auto slot = [&](int u) {
+            const int64_t k = i + u * step <= last ? i + u * step : last;
+            return a.partials + (k == 0 ? 2 * c + 1 : 2 * (c + k)) * a.dim;
+        };
+        if (whole) {
 #pragma unroll
-        for (int u = 0; u < JOIN_UNROLL; ++u) r[u] = load_partial8(a, c, i + u * step <= last ? i + u * step : last, e);
+            for (int u = 0; u < JOIN_UNROLL; ++u) r[u] = load_raw8<G_F32>(slot(u), from);
+        } else {
+#pragma unroll
+            for (int u = 0; u < JOIN_UNROLL; ++u) r[u] = load_narrow8<G_F32>(slot(u), a.dim);
+        }
 #pragma unroll
         for (int u = 0; u < JOIN_UNROLL; ++u)
             if (i + u * step <= last)
@@ -735,14 +755,23 @@ __global__ __launch_bounds__(JOIN_BLOCK) void embedding_join(SumArgs a) {
         const uint32_t end = a.keys[next - 1], begin = a.keys[base], before = a.keys[base > 0 ? base - 1 : 0];
         const bool earlier = base > 0 && begin == key && before == key;
         if (key < static_cast<uint32_t>(a.rows) && end == key && !earlier) {
-            for (;;) {
-                const int64_t k = next + (reach + lane) * a.chunk;
-                const uint64_t on = __ballot(k < a.n && a.keys[k < a.n ? k : 0] == key);
-                if (on != ~uint64_t(0)) {
-                    reach += __builtin_ctzll(~on);
-                    break;
+            // the ids are sorted: behind the nearest 64 chunks, each round
+            // narrows the place where the run ends to a 64th
+            const auto reached = [&](int64_t i) {
+                const int64_t k = next + i * a.chunk;
+                return __ballot(k < a.n && a.keys[k < a.n ? k : 0] == key);
+            };
+            const uint64_t near = reached(lane);
+            reach = ~near ? __builtin_ctzll(~near) : 64;
+            if (reach == 64) {
+                int64_t off = a.chunks - c;  // the run reaches `reach` chunks, not `off`
+                while (off - reach > 1) {
+                    const int64_t step = (off - reach + 63) / 64;
+                    const int64_t i = reach + (lane + 1) * step - 1;
+                    const uint64_t on = reached(i);
+                    reach += (~on ? __builtin_ctzll(~on) : 64) * step;
+                    off = reach + step < off ? reach + step : off;
                 }
-                reach += 64;
             }
         }
     }
@@ -773,11 +802,12 @@ __global__ __launch_bounds__(JOIN_BLOCK) void embedding_join(SumArgs a) {
 
 // A list of at most FEW_MAX tokens whose rows are at most FEW_SUMS column
 // tiles is summed without a sort.  One launch instead of three: 511 x 2048
-// FP16 added into 32000 rows take 9.9 us a call, against 16.6.  Every
-// workgroup reads all ids, which is what more tokens or tiles cost: 4096
-// tiles take 9.0 us against 14.7, 8192 take 15.5 against 14.9; one id in
-// all of 512 tokens takes 14.6 against 14.9, of 1024 tokens 26 against 18.5.
-// Eight waves a workgroup instead of four: 9.2 against 7.6 us at 2044 tiles.
+// FP16 added into 32000 rows take 9.9 us a call, against 16.6 (the kernel
+// 6.6, against 14.6).  Every workgroup reads all ids, which is what more
+// tokens or tiles cost: 4096 tiles take 9.0 us against 14.7, 8192 take 15.5
+// against 14.9; one id in all of 512 tokens takes 14.6 against 14.9, of 1024
+// tokens 26 against 18.5.  Eight waves a workgroup instead of four: 9.2
+// against 7.6 us at 2044 tiles.
 constexpr int FEW_MAX = 512;
 constexpr int64_t FEW_SUMS = 4096;
 constexpr int FEW_BLOCK = 256;
@@ -789,12 +819,13 @@ constexpr int64_t FEW_FLAGS = 4096;
 // Tokens of one id that a single wave sums, all in flight at once.
 constexpr int FEW_ALONE = SUM_UNROLL;
 
-// Sum of the rows list[begin .. end), columns [e, e + 8), in that order.  The
+// Sum of the rows list[begin .. end), the lane's eight columns, in that order.  The
 // last group reads its last row again for what it lacks.
 template <int GDT>
 __device__ __forceinline__ f32x8 sum_list(const SumArgs &a, const uint16_t *list, int begin, int end, int64_t e) {
     f32x8 acc = 0.0f;
-    const bool whole = e + 8 <= a.dim;
+    const bool whole = a.dim >= 8;
+    const int64_t from = first_of_eight(e, a.dim);
     for (int j = begin; j < end; j += SUM_UNROLL) {
         Raw8<GDT> raw[SUM_UNROLL];
         const auto source = [&](int u) {
@@ -803,10 +834,10 @@ __device__ __forceinline__ f32x8 sum_list(const SumArgs &a, const uint16_t *list
         };
         if (whole) {
 #pragma unroll
-            for (int u = 0; u < SUM_UNROLL; ++u) raw[u] = load_raw8<GDT>(source(u), e);
+            for (int u = 0; u < SUM_UNROLL; ++u) raw[u] = load_raw8<GDT>(source(u), from);
         } else {
 #pragma unroll
-            for (int u = 0; u < SUM_UNROLL; ++u) raw[u] = load_edge8<GDT>(source(u), e, a.dim);
+            for (int u = 0; u < SUM_UNROLL; ++u) raw[u] = load_narrow8<GDT>(source(u), a.dim);
         }
 #pragma unroll
         for (int u = 0; u < SUM_UNROLL; ++u) {
@@ -861,7 +892,7 @@ __global__ __launch_bounds__(FEW_BLOCK) void embedding_grad_few(SumArgs a, SortK
     Raw8<GDT> own;  // wave 0: token t's row, needed unless an earlier token has the id
     if (wave == 0 && on) {
         const char *row = static_cast<const char *>(a.grad_out) + int64_t(t) * a.grad_stride * elem_bytes<GDT>;
-        own = e + 8 <= a.dim ? load_raw8<GDT>(row, e) : load_edge8<GDT>(row, e, a.dim);
+        own = a.dim >= 8 ? load_raw8<GDT>(row, first_of_eight(e, a.dim)) : load_narrow8<GDT>(row, a.dim);
     }
     const int64_t id = load_index(s.ids, s.wide_ids, t);
     if (id < 0 || id >= s.rows || id == s.padding_id) return;

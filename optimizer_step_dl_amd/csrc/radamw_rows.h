@@ -90,6 +90,14 @@ __device__ __forceinline__ float chunk_value(u32x4 c, int j) {
     }
 }
 
+// A row of at least eight values is cut into eights, a lane to each; where
+// they do not go up evenly, the last lane serves the row's last eight values,
+// some of them beside the lane before it, so that no lane moves values one by
+// one.  Only rows of fewer than eight take e itself.
+__device__ __forceinline__ int64_t first_of_eight(int64_t e, int64_t dim) {
+    return e + 8 <= dim || dim < 8 ? e : dim - 8;
+}
+
 // Eight consecutive values at element e.
 template <int DT>
 struct Raw8 {
