@@ -62,7 +62,13 @@ __device__ __forceinline__ double label_logp(float at_label, float shift, double
 constexpr double SUM_LIMIT = 0x1p60;
 
 // Rows whose exponents are shifted by c = fl(m * LOG2E).
-__device__ __forceinline__ bool shiftable(float top) { return fabsf(top) < 16777216.0f; }
+constexpr float SHIFT_LIMIT = 16777216.0f;
+__device__ __forceinline__ bool shiftable(float top) { return fabsf(top) < SHIFT_LIMIT; }
+
+// Rows that lanes with a shift each may sum: the values of a lane that has
+// none, all at most -2^24, are left out of the sum, which is right where the
+// row's maximum exceeds them by 256 or more (e^-256 of it, each).
+__device__ __forceinline__ bool shiftable_by_lane(float top) { return shiftable(top) && top >= 256.0f - SHIFT_LIMIT; }
 
 // exp2(x * LOG2E - c).  LOG2E alone is off by 1.3e-8, which changes p_j by
 // that much of x and logp by 1.3e-8 (x_a - mean x); EXACT adds the rest of
@@ -436,8 +442,9 @@ __global__ __launch_bounds__(STREAM_BLOCK) void loss_rows_long(LogitsArgs x, ROW
     const RowShape<DT> s(in, x.vocab);
     const float at_label = load_value<DT>(in, label);
     // top: the lane's largest value so far; shift: what its sum is relative
-    // to.  A lane that holds something else than a number, or a value too
-    // large to shift by, makes `top` of the row such a one, and the row slow.
+    // to.  A value of 2^24 or more makes the row's maximum such a one, and the
+    // row slow; a lane whose values are all -2^24 or less adds nothing, and the
+    // row is slow unless its maximum is far above; a NaN makes the sum one.
     float top = -__builtin_inff(), shift = 0.0f;
     double sum = 0.0;
     const auto take = [&](const u32x4 (&c)[U]) {
@@ -475,7 +482,7 @@ __global__ __launch_bounds__(STREAM_BLOCK) void loss_rows_long(LogitsArgs x, ROW
         shift = to;
     }
     const float all = block_max<NT>(top, sh.tops);
-    if (!shiftable(all)) {
+    if (!shiftable_by_lane(all)) {
         slow_row<DT, NT, GRAD>(x, f, row, label, sh);
         return;
     }
