@@ -45,6 +45,11 @@ def _flat32(t: Optional[torch.Tensor], what: str, n: int) -> Optional[torch.Tens
     return t.detach().reshape(-1).to(torch.float32).contiguous()
 
 
+def _empty32(shape, device) -> torch.Tensor:
+    """An FP32 output, whatever torch's default dtype."""
+    return torch.empty(shape, dtype=torch.float32, device=device)
+
+
 # --------------------------------------------------------------- embedding --
 
 class _Embedding(torch.autograd.Function):
@@ -108,9 +113,7 @@ class _PolicyLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, labels, old_logp, ref_logp, advantages, weights, opts):
         n, dev = logits.shape[0], logits.device
-        total = torch.empty((), device=dev)
-        loss, logp = torch.empty(n, device=dev), torch.empty(n, device=dev)
-        stats = torch.empty((n, 4), device=dev)
+        total, loss, logp, stats = (_empty32(s, dev) for s in ((), n, n, (n, 4)))
         _abi.radamw_policy_loss(logits.detach(), labels, old_logp, advantages, opts, total, loss, logp,
                                 ref_logp=ref_logp, weights=weights, row_stats=stats)
         ctx.save_for_backward(logits, labels, stats)
@@ -128,9 +131,7 @@ class _PreferenceLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, labels, offsets, ref_logp, weights, opts):
         n, dev, pairs = logits.shape[0], logits.device, weights.numel()
-        total = torch.empty((), device=dev)
-        loss, seq_logp = torch.empty(pairs, device=dev), torch.empty(2 * pairs, device=dev)
-        logp, stats = torch.empty(n, device=dev), torch.empty((n, 4), device=dev)
+        total, loss, seq_logp, logp, stats = (_empty32(s, dev) for s in ((), pairs, 2 * pairs, n, (n, 4)))
         _abi.radamw_preference_loss(logits.detach(), labels, offsets, ref_logp, opts, total, loss, seq_logp, logp,
                                     stats, weights=weights)
         ctx.save_for_backward(logits, labels, stats)
@@ -198,7 +199,7 @@ def preference_loss(logits: torch.Tensor, labels: torch.Tensor, offsets: torch.T
         raise ValueError(f"offsets must hold 2 * pairs + 1 entries (got {offsets.numel()})")
     pairs = offsets.numel() // 2
     if weights is None:
-        w = torch.full((pairs,), 1.0 / pairs, device=logits.device)
+        w = torch.full((pairs,), 1.0 / pairs, dtype=torch.float32, device=logits.device)
     else:
         w = _flat32(weights, "weights", pairs)
     return _PreferenceLoss.apply(_rows(logits), flat, offsets.to(flat.dtype).contiguous(),
