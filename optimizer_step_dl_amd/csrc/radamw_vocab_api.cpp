@@ -161,7 +161,10 @@ int radamw_embedding_grad(const void *grad_out, radamw_dtype grad_dtype, int64_t
     if (rows == 0 || (n == 0 && accumulate)) return RADAMW_OK;
     const EmbeddingPlan plan = embedding_plan(n, rows, dim);
     if (workspace_bytes < plan.bytes) return RADAMW_ERR_RANGE;
-    if (plan.chunks > LAUNCH_MAX_BLOCKS || plan.sum_blocks > LAUNCH_MAX_BLOCKS) return RADAMW_ERR_RANGE;
+    // the sums' grid is the largest: a chunk holds 64 tokens at these sizes, so
+    // that the join has at most 2^25 / 8 workgroups of 512 lanes and the sort
+    // 2^20 tiles beside 2^20 that clear
+    if (plan.sum_blocks > LAUNCH_MAX_BLOCKS) return RADAMW_ERR_RANGE;
     int dev;
     if ((rc = stream_device(stream, &dev))) return rc;
     DeviceScope scope(dev);
