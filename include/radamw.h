@@ -687,8 +687,11 @@ int radamw_embedding_grad(const void *grad_out, radamw_dtype grad_dtype, int64_t
  *                loss alone.  May be exactly the logits (same pointer and
  *                stride), which it then replaces.
  * Everything per row is formed in FP64 from the row's sum of exponentials
- * (FP32 by lane, joined in FP64).  Where the gradient is asked
- * for, the logits of rows up to 256 KiB are read once.
+ * (FP32 by lane, joined in FP64); the total adds the FP32 losses in FP64.
+ * Where the gradient is asked for, the logits of rows up to 256 KiB are read
+ * once, by another kernel than without: logp, loss and total then agree to
+ * the rounding of the sum of exponentials (about 1e-7 of it), not bit for
+ * bit.  A ratio that shall be exactly 1 is had by old_logp = NULL.
  */
 typedef struct {
     double clip_low;

@@ -1,12 +1,15 @@
 """GPU tests of the losses where a row's exponents or its sum are hard to
 hold: against the plain 64-bit forms, with and without the gradient (which
 take different kernels)."""
+import math
+
 import pytest
 import torch
 
 import optimizer_step_dl_amd as ra
 from gpu_helpers import announce
 from test_gpu_losses import check_policy, check_preference, gen
+from vocab_helpers import U, Rows, close
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +42,67 @@ def test_rows_on_both_sides_of_the_lowest_shift(vocab):
     assert abs(float(o["logp"][0]) - float(plain)) < 1e-5 * abs(float(plain))
     check_preference(x, labels, torch.ones(n, dtype=torch.bool), [0, 4, n], torch.tensor([-30.0, -20.0]),
                      ra.preference_options(0.1, 0.1))
+
+
+@pytest.mark.parametrize("dtype,vocab", [(F32, 1000), (F32, 12_000), (F32, 50_001), (F32, 70_000), (torch.bfloat16, 131_072),
+                                         (torch.float16, 3001)])
+def test_exponents_carry_all_of_log2_e(dtype, vocab):
+    """One logit stands g above the label and far above the rest, so that
+    logp = -g to 1e-12 and an exponent's factor that is off by a relative d
+    moves it by d g.  The policy loss -exp(logp - old) shows logp as it is
+    before it is rounded.
+
+    The bound: the exponents are exact to 2^-40 (the shift cancels), v_exp_f32
+    is within 1 ulp (2 u), the loss is rounded once (u); 1 u for the rest.
+    FP32's log2 e alone (d = 1.3e-8) gives 9 to 18 u here."""
+    announce(f"exponents {dtype} vocab={vocab}")
+    n = 24
+    x = torch.zeros((n, vocab), dtype=dtype)
+    g = torch.linspace(42, 84, n).to(dtype)
+    labels = (torch.arange(n) * 37 + vocab // 3) % vocab
+    rows = torch.arange(n)
+    x[rows, (labels + vocab // 2) % vocab] = g
+    if vocab > 10_000:  # leading columns that serve no shift
+        x[::4, :9000] = float("-inf")
+        labels[::4] = vocab - 3
+        x[rows[::4], labels[::4]] = 0.0
+        x[::4, -9] = g[::4]
+    r = Rows(x, labels, torch.ones(n, dtype=torch.bool))
+    old = r.logp.float()
+    want = -(r.logp - old.double()).exp()
+    d = "cuda"
+    for grad in (False, True):
+        total, loss, logp = torch.empty((), device=d), torch.empty(n, device=d), torch.empty(n, device=d)
+        xd = x.to(d)
+        ra.radamw_policy_loss(xd, labels.to(d), old.to(d), torch.ones(n, device=d), ra.policy_options(), total, loss,
+                              logp, grad=xd if grad else None)
+        close(loss, want, 3 * U * want.abs(), f"loss, grad={grad}")  # close adds the rounding itself
+        close(logp, r.logp, 3 * U, f"logp, grad={grad}")
+
+
+@pytest.mark.parametrize("dtype", [F32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("vocab", [4096, 16_384])
+def test_log_probabilities_are_off_to_no_side(dtype, vocab):
+    """Errors of one sign add up over a sequence: the mean error of logp over
+    N rows, from losses -exp(logp - old).
+
+    The bound: a row's error is the rounding of the label's exponent (up to 8:
+    2^-21 / 2 log 2 = 1.7e-7 at most, 1e-7 in the mean square), of a lane's
+    chain (5e-8) and of the loss (3e-8): 1.2e-7 in the mean square, and four
+    times that over sqrt N; v_exp_f32 is 3.4e-9 low in the mean."""
+    announce(f"mean error {dtype} vocab={vocab}")
+    n = 4096
+    x = 2 * torch.randn((n, vocab), generator=gen(vocab))
+    labels = torch.randint(0, vocab, (n,), generator=gen(3))
+    x[torch.arange(n), labels] += 4 + 6 * torch.rand(n, generator=gen(4))
+    xd = x.to(dtype).cuda()
+    z = xd.double()
+    logp = z.gather(1, labels.cuda()[:, None])[:, 0] - z.logsumexp(1)
+    old = logp.float()
+    bound = 4 * 1.2e-7 / math.sqrt(n) + 3.4e-9
+    for grad in (False, True):
+        total, loss, out = (torch.empty(s, device="cuda") for s in ((), n, n))
+        ra.radamw_policy_loss(xd, labels.cuda(), old, torch.ones(n, device="cuda"), ra.policy_options(), total, loss,
+                              out, grad=torch.empty_like(xd) if grad else None)
+        off = float((loss.double() / -(logp - old.double()).exp() - 1).mean())
+        assert abs(off) <= bound, (grad, off, bound)
