@@ -23,8 +23,8 @@
 // once.  A workgroup holds a whole row in registers (up to 256 KiB: 1024
 // lanes x 16 chunks of 16 bytes), so that the sum and the gradient need one
 // read; longer rows are read twice.  m is the largest of the row's first
-// NT chunks, so the exponentials are summed while the other chunks are still
-// arriving.
+// NT chunks and the label's logit, so the exponentials are summed while the
+// other chunks are still arriving.
 #include "radamw_rows.h"
 #include "radamw_vocab.h"
 
@@ -50,12 +50,6 @@ __device__ __forceinline__ double wave_sum(double v) {
 
 constexpr double LN2 = 0.6931471805599453;
 constexpr double LOG2E_64 = 1.4426950408889634;
-
-// logp of a label's logit, from a sum of exp_sum's exponentials relative to
-// the shift.
-__device__ __forceinline__ double label_logp(float at_label, float shift, double sum) {
-    return (double(at_label) * LOG2E_64 - double(shift)) * LN2 - log(sum);
-}
 
 // Sums below this have no exponential near FP32's largest value, and their
 // reciprocals times a coefficient none near its smallest.
@@ -134,18 +128,18 @@ struct RowShape {
     }
     // Value number of chunk k's first value.
     __device__ __forceinline__ int64_t chunk_at(int64_t k) const { return head + k * E; }
+    // The chunk of value v, or -1 for an edge.
+    __device__ __forceinline__ int chunk_of(int v) const { return v >= head && v < tail_at ? (v - head) / E : -1; }
     // The edge value lane t holds, or -1: the head from lane 0 on, the tail
-    // from lane 64 on.
-    __device__ __forceinline__ int edge(int t) const {
+    // from lane 64 on, and from lane 128 on the values of chunk `apart`, which
+    // is then no lane's chunk (-1: none).
+    __device__ __forceinline__ int edge(int t, int apart) const {
         if (t < 64) return t < head ? t : -1;
-        const int e = tail_at + (t - 64);
-        return e < vocab ? e : -1;
-    }
-    // The lane (of a workgroup of nt) that stores value v.
-    __device__ __forceinline__ int lane_of(int64_t v, int nt) const {
-        if (v < head) return static_cast<int>(v);
-        if (v >= tail_at) return 64 + static_cast<int>(v - tail_at);
-        return static_cast<int>((v - head) / E) % nt;
+        if (t < 128) {
+            const int e = tail_at + (t - 64);
+            return e < vocab ? e : -1;
+        }
+        return apart >= 0 && t < 128 + E ? head + apart * E + (t - 128) : -1;
     }
 };
 
@@ -167,7 +161,7 @@ __device__ __forceinline__ void zero_row(void *row, int64_t vocab) {
     const u32x4 z = {0, 0, 0, 0};
     const RowShape<DT> s(row, vocab);
     for (int k = threadIdx.x; k < s.full; k += NT) stream_out<DT>(row, s.chunk_at(k), z);
-    const int e = s.edge(threadIdx.x);
+    const int e = s.edge(threadIdx.x, -1);
     if (e >= 0) store_value<DT>(row, e, 0.0f);
 }
 
@@ -244,11 +238,39 @@ __device__ __forceinline__ void absent_row(const ROW &f, const LogitsArgs &x, in
     }
 }
 
-// The sum that goes with the gradient's exponentials, from one of exp_sum's
-// relative to `top`: what LOG2E lacks of m is taken out again (that of x - m
-// is below the exponent's rounding).
-__device__ __forceinline__ double record_sum(double sum, float top) {
-    return sum * exp2(-double(top) * (LOG2E_64 - double(LOG2E)));
+// The label's own exponential, formed in binary64: the label is most of many
+// a row's sum, and an FP32 sum that held it would leave few digits of the
+// others, that is of logp and 1 - p where p is near 1 (8.5863e-5 for a logp of
+// 8.5831e-5).  It takes no time that shows (770 us against 768 for 8192 x
+// 131072 BF16).
+struct LabelTerm {
+    double log2;     // of the exponential
+    double inverse;  // 1 / the exponential
+    double own;      // the exponential
+    double factor;   // to the sum that goes with the gradient's exponentials
+};
+
+// By a whole wave, relative to the shift c of `top` (`shifted`) or to `top`
+// itself.  The gradient's exponentials lack what LOG2E does: the part of m is
+// taken out of their sum (that of x - m is below the exponent's rounding).
+// The three exponentials are evaluated at once, by lanes 0, 1 and 2.
+__device__ __forceinline__ LabelTerm label_term(float at_label, float top, float c, bool shifted) {
+    const int lane = threadIdx.x & 63;
+    const double t = shifted ? double(at_label) * LOG2E_64 - double(c) : (double(at_label) - double(top)) * LOG2E_64;
+    const double lacks = shifted ? -double(top) * (LOG2E_64 - double(LOG2E)) : 0.0;
+    const double e = exp2(lane == 0 ? t : lane == 1 ? -t : lacks);
+    return {t, __shfl(e, 1, 64), __shfl(e, 0, 64), __shfl(e, 2, 64)};
+}
+
+struct RowSum {
+    double logp;
+    double of_grad;
+};
+__device__ __forceinline__ RowSum with_label(double others, const LabelTerm &l) {
+    const double sum = others + l.own;
+    // an exponential below 2^-500 adds nothing to the others, which hold m's
+    const double logp = l.log2 > -500.0 ? -log1p(others * l.inverse) : l.log2 * LN2 - log(sum);
+    return {logp, sum * l.factor};
 }
 
 // The row's scalars from its maximum, log-probability and sum, by a whole
@@ -335,15 +357,13 @@ __device__ __forceinline__ void slow_row(const LogitsArgs &x, const ROW &f, int6
 #pragma clang loop unroll(disable)
     for (int64_t k = threadIdx.x; k < x.vocab; k += NT) {
         const float z = load_value<DT>(in, k);
-        sum += double(shifted ? exp_sum(z, to) : exp_neg(z - top));
+        if (k != label) sum += double(shifted ? exp_sum(z, to) : exp_neg(z - top));
     }
     sum = block_sum<NT>(sum, sh.sums);
     if (threadIdx.x < 64) {
-        const double logp = shifted ? label_logp(at_label, shift, sum)
-                                    : (double(at_label) - double(top)) - log(sum);
-        const double of_grad = shifted ? record_sum(sum, top) : sum;
-        const RowResult r = finish_row(f, x, row, top, of_grad, logp);
-        if (GRAD && threadIdx.x == 0) put_factors(sh, r, x.grad_scale, of_grad);
+        const RowSum w = with_label(sum, label_term(at_label, top, shift, shifted));
+        const RowResult r = finish_row(f, x, row, top, w.of_grad, w.logp);
+        if (GRAD && threadIdx.x == 0) put_factors(sh, r, x.grad_scale, w.of_grad);
     }
     if constexpr (GRAD) {
         char *out = static_cast<char *>(x.grad) + row * x.grad_stride * elem_bytes<DT>;
@@ -377,21 +397,25 @@ __global__ __launch_bounds__(NT) void loss_rows(LogitsArgs x, ROW f) {
     const RowShape<DT> s(in, x.vocab);
     const int used = (s.full + NT - 1) / NT;  // chunks of the busiest lane
     const float at_label = load_value<DT>(in, label);
+    // the label's chunk is held value by value, and its value left out of the sum
+    const int apart = s.chunk_of(static_cast<int>(label));
     u32x4 c[CH];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
         const int k = tid + i * NT;
-        if (k < s.full) c[i] = stream_chunk<DT>(in, s.chunk_at(k));
+        if (k < s.full && k != apart) c[i] = stream_chunk<DT>(in, s.chunk_at(k));
         else c[i] = lowest_chunk<DT>();
     }
-    const int edge = s.edge(tid);
-    const float at_edge = edge >= 0 ? load_value<DT>(in, edge) : -__builtin_inff();
+    const int edge = s.edge(tid, apart);
+    const float at_edge = edge >= 0 && edge != label ? load_value<DT>(in, edge) : -__builtin_inff();
     float top = at_edge;
 #pragma unroll
     for (int j = 0; j < E; ++j) top = fmaxf(top, chunk_value<DT>(c[0], j));
-    top = block_max<NT>(top, sh.tops);
+    top = fmaxf(block_max<NT>(top, sh.tops), at_label);
     const Shift to = shift_by(top);
     const float shift = to.c;
+    LabelTerm own{};  // while the row is still arriving
+    if (wave == 0) own = label_term(at_label, top, shift, true);
     float part[4] = {exp_sum(at_edge, to), 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
@@ -406,10 +430,9 @@ __global__ __launch_bounds__(NT) void loss_rows(LogitsArgs x, ROW f) {
         return;
     }
     if (wave == 0) {
-        const double logp = label_logp(at_label, shift, sum);
-        const double of_grad = record_sum(sum, top);
-        const RowResult r = finish_row(f, x, row, top, of_grad, logp);
-        if (GRAD && tid == 0) put_factors(sh, r, x.grad_scale, of_grad);
+        const RowSum w = with_label(sum, own);
+        const RowResult r = finish_row(f, x, row, top, w.of_grad, w.logp);
+        if (GRAD && tid == 0) put_factors(sh, r, x.grad_scale, w.of_grad);
     }
     if constexpr (GRAD) {
         __syncthreads();
@@ -425,12 +448,10 @@ __global__ __launch_bounds__(NT) void loss_rows(LogitsArgs x, ROW f) {
                 float v[E];
 #pragma unroll
                 for (int j = 0; j < E; ++j) v[j] = exp_shifted(chunk_value<DT>(c[i], j), shift) * k;
-                if (at < s.full) store_values<DT>(out, s.chunk_at(at), v);
+                if (at < s.full && at != apart) store_values<DT>(out, s.chunk_at(at), v);
             }
         }
-        if (edge >= 0) store_value<DT>(out, edge, exp_shifted(at_edge, shift) * k);
-        // the label's value, behind its own lane's store of what holds it
-        if (tid == s.lane_of(label, NT)) store_value<DT>(out, label, sh.at_label);
+        if (edge >= 0) store_value<DT>(out, edge, edge == label ? sh.at_label : exp_shifted(at_edge, shift) * k);
     }
 }
 
@@ -485,15 +506,16 @@ __global__ __launch_bounds__(STREAM_BLOCK) void loss_rows_long(LogitsArgs x, ROW
         top = t;
         shift = to.c;
     };
-    const int edge = s.edge(tid);
-    const float at_edge = edge >= 0 ? load_value<DT>(in, edge) : -__builtin_inff();
+    const int apart = s.chunk_of(static_cast<int>(label));  // as in loss_rows
+    const int edge = s.edge(tid, apart);
+    const float at_edge = edge >= 0 && edge != label ? load_value<DT>(in, edge) : -__builtin_inff();
     for (int k0 = 0; k0 < s.full; k0 += NT * U) {
         u32x4 c[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int k = k0 + u * NT + tid;
-            if (k < s.full) c[u] = GRAD ? load_chunk<DT>(in, s.chunk_at(k)) : stream_chunk<DT>(in, s.chunk_at(k));
-            else c[u] = lowest_chunk<DT>();
+            if (k >= s.full || k == apart) c[u] = lowest_chunk<DT>();
+            else c[u] = GRAD ? load_chunk<DT>(in, s.chunk_at(k)) : stream_chunk<DT>(in, s.chunk_at(k));
         }
         take(c);
     }
@@ -504,7 +526,7 @@ __global__ __launch_bounds__(STREAM_BLOCK) void loss_rows_long(LogitsArgs x, ROW
         top = t;
         shift = to.c;
     }
-    const float all = block_max<NT>(top, sh.tops);
+    const float all = fmaxf(block_max<NT>(top, sh.tops), at_label);
     if (!shiftable_by_lane(all)) {
         slow_row<DT, NT, GRAD>(x, f, row, label, sh);
         return;
@@ -513,10 +535,9 @@ __global__ __launch_bounds__(STREAM_BLOCK) void loss_rows_long(LogitsArgs x, ROW
     sum = block_sum<NT>(rescaled(sum, shift, to), sh.sums);
     shift = to;
     if (wave == 0) {
-        const double logp = label_logp(at_label, shift, sum);
-        const double of_grad = record_sum(sum, all);
-        const RowResult r = finish_row(f, x, row, all, of_grad, logp);
-        if (GRAD && tid == 0) put_factors(sh, r, x.grad_scale, of_grad);
+        const RowSum w = with_label(sum, label_term(at_label, all, shift, true));
+        const RowResult r = finish_row(f, x, row, all, w.of_grad, w.logp);
+        if (GRAD && tid == 0) put_factors(sh, r, x.grad_scale, w.of_grad);
     }
     if constexpr (GRAD) {
         __syncthreads();
@@ -530,20 +551,19 @@ __global__ __launch_bounds__(STREAM_BLOCK) void loss_rows_long(LogitsArgs x, ROW
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int at = k0 + u * NT + tid;
-                if (at < s.full) c[u] = stream_chunk<DT>(in, s.chunk_at(at));
+                if (at < s.full && at != apart) c[u] = stream_chunk<DT>(in, s.chunk_at(at));
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int at = k0 + u * NT + tid;
-                if (at >= s.full) continue;
+                if (at >= s.full || at == apart) continue;
                 float v[E];
 #pragma unroll
                 for (int j = 0; j < E; ++j) v[j] = exp_shifted(chunk_value<DT>(c[u], j), shift) * k;
                 store_values<DT>(out, s.chunk_at(at), v);
             }
         }
-        if (edge >= 0) store_value<DT>(out, edge, exp_shifted(at_edge, shift) * k);
-        if (tid == s.lane_of(label, NT)) store_value<DT>(out, label, sh.at_label);
+        if (edge >= 0) store_value<DT>(out, edge, edge == label ? sh.at_label : exp_shifted(at_edge, shift) * k);
     }
 }
 
@@ -574,7 +594,7 @@ __global__ __launch_bounds__(GRAD_BLOCK) void logits_grad(LogitsArgs x, const fl
     // x - m first where the forward pass summed so
     const bool shifted = dead || shiftable(r.max);
     const float shift = dead ? 0.0f : r.max * LOG2E;
-    const int edge = blockIdx.y == 0 ? s.edge(tid) : -1;
+    const int edge = blockIdx.y == 0 ? s.edge(tid, -1) : -1;
     if (edge >= 0) {
         const float z = dead ? -__builtin_inff() : load_value<DT>(in, edge);
         const float v = (shifted ? exp_shifted(z, shift) : exp_neg(z - r.max)) * k;

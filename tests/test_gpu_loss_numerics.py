@@ -106,3 +106,46 @@ def test_log_probabilities_are_off_to_no_side(dtype, vocab):
                               out, grad=torch.empty_like(xd) if grad else None)
         off = float((loss.double() / -(logp - old.double()).exp() - 1).mean())
         assert abs(off) <= bound, (grad, off, bound)
+
+
+@pytest.mark.parametrize("dtype", [F32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("vocab", [3, 1000, 4097, 30_000, 50_001, 140_000])
+def test_confident_rows_keep_their_digits(dtype, vocab):
+    """Labels 10 to 40 above the rest, so that 1 - p goes down to e^-28 and
+    less, in chunks and at the row's edges: logp = -log(1 + r), r the others'
+    sum over the label's exponential, to the digits of r; likewise the label's
+    gradient c (1 - p).
+
+    The bound: an exponential is off by 3 u |y| + 2 u (|y| < 50 here), a
+    lane's chain by its length, logp and the gradient are rounded (close) and
+    the factor of the gradient is an FP32 value."""
+    announce(f"confident {dtype} vocab={vocab}")
+    n = 24
+    x = torch.randn((n, vocab), generator=gen(vocab)).to(dtype)
+    labels = (torch.arange(n) * (vocab // n) + torch.arange(n) % 3) % vocab
+    labels[-1], labels[-2] = vocab - 1, 0
+    x[torch.arange(n), labels] = torch.linspace(10, 40, n).to(dtype)
+    z = x.double()
+    others = z.clone()
+    others[torch.arange(n), labels] = float("-inf")
+    r = (others - z.gather(1, labels[:, None])).exp().sum(1)
+    logp, less = -r.log1p(), r / (1 + r)
+    chain = math.ceil(math.ceil(vocab / 256) / 4) + 8
+    rel = (3 * 50 + 2 + chain) * U
+    d = "cuda"
+    adv = torch.linspace(0.5, 2, n)
+    for grad in (False, True):
+        total, loss, out = (torch.empty(s, device=d) for s in ((), n, n))
+        stats, g = torch.empty((n, 4), device=d), torch.empty((n, vocab), dtype=dtype, device=d)
+        xd, ld = x.to(d), labels.to(d)
+        ra.radamw_policy_loss(xd, ld, None, adv.to(d), ra.policy_options(), total, loss, out, row_stats=stats,
+                              grad=g if grad else None, grad_scale=1024.0)
+        close(out, logp, rel * logp.abs(), f"logp, grad={grad}")
+        if not grad:
+            ra.radamw_logits_grad(xd, ld, stats, g, grad_scale=1024.0)
+        want = -1024 * adv.double() * less
+        close(g.gather(1, ld[:, None])[:, 0], want, (rel + 4 * U) * want.abs(), f"label's gradient, fused={grad}")
+    loss, seq, lp = torch.empty(n // 2, device=d), torch.empty(n, device=d), torch.empty(n, device=d)
+    ra.radamw_preference_loss(x.to(d), labels.to(d), torch.arange(n + 1, device=d), torch.zeros(n, device=d),
+                              ra.preference_options(), torch.empty((), device=d), loss, seq, lp, stats)
+    close(seq, logp, rel * logp.abs(), "seq_logp")
