@@ -149,3 +149,26 @@ def test_confident_rows_keep_their_digits(dtype, vocab):
     ra.radamw_preference_loss(x.to(d), labels.to(d), torch.arange(n + 1, device=d), torch.zeros(n, device=d),
                               ra.preference_options(), torch.empty((), device=d), loss, seq, lp, stats)
     close(seq, logp, rel * logp.abs(), "seq_logp")
+
+
+@pytest.mark.parametrize("dtype,vocab", [(F32, 30_000), (torch.bfloat16, 100_000), (torch.float16, 12_000),
+                                         (torch.bfloat16, 140_000)])
+def test_rows_whose_maximum_is_far_from_every_early_column(dtype, vocab):
+    """The first columns and those around the label are masked by -inf or lie
+    45 to 3000 below the others: the exponentials relative to the largest of
+    them leave the range, and the row's maximum is found first."""
+    announce(f"far maximum {dtype} {vocab}")
+    lows = [-45.0, -60.0, -100.0, -3000.0]
+    n = len(lows) + 1
+    x = torch.randn((n, vocab), generator=gen(vocab)).to(dtype)
+    labels = torch.full((n,), vocab - 20)
+    for i, low in enumerate(lows):
+        x[i, :9000] = low
+        x[i, vocab - 40:] = low
+    x[4, :9000] = float("-inf")
+    x[4, vocab - 40:] = float("-inf")
+    x[4, labels[4]] = -70.0
+    adv = torch.randn(n, generator=gen(18))
+    taken = torch.ones(n, dtype=torch.bool)
+    check_policy(x, labels, taken, None, adv, ra.policy_options(), scale=8.0)
+    check_preference(x, labels, taken, [0, 2, n], torch.tensor([-40.0, -50.0]), ra.preference_options(0.01, 0.1))
