@@ -109,7 +109,8 @@ __device__ __forceinline__ u32x4 lowest_chunk() {
 // lane.  A row of 16-bit values may start at any even address; 16-byte
 // accesses from an odd multiple of two bytes cost 17% of the fused loss
 // (4097 rows of 50001 FP16 logits: 157 us, against 134 us for 50000), those
-// from a cache line 6% less than from elsewhere (50048: 125 us).
+// from a cache line 6% less than from elsewhere (50048: 125 us).  Cut this way
+// the three take the same.
 template <int DT>
 struct RowShape {
     static constexpr int E = chunk_elems<DT>;
