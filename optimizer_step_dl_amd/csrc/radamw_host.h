@@ -8,6 +8,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <map>
@@ -153,6 +154,83 @@ inline int check_alias(std::vector<Range> &v) {
         if (r.written) end_written = std::max(end_written, r.hi);
     }
     return RADAMW_OK;
+}
+
+// ------------------------------------------------------ arrays of rows --
+
+// Largest row, token and vocabulary counts: they index with 31 bits.
+constexpr int64_t MAX_ROWS = 0x7ffffff0;
+
+// The buffers of one call: each is queried once per allocation, and written
+// ranges may overlap nothing.
+class Buffers {
+  public:
+    explicit Buffers(int dev) : dev_(dev) {}
+
+    int add(const void *p, size_t align, int64_t bytes, bool written) {
+        if (bytes <= 0) return RADAMW_OK;
+        if (!p) return RADAMW_ERR_INVALID;
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+        if (a % align != 0) return RADAMW_ERR_ALIGN;
+        const uintptr_t end = a + static_cast<uintptr_t>(bytes);
+        if (end < a) return RADAMW_ERR_INVALID;
+        bool known = false;
+        for (int i = 0; i < extents_; ++i) {
+            if (a < extent_[i].lo || a >= extent_[i].hi) continue;
+            if (end > extent_[i].hi) return RADAMW_ERR_INVALID;
+            known = true;
+            break;
+        }
+        if (!known) {
+            uintptr_t lo = 0, hi = 0;
+            const int rc = query_extent(dev_, p, &lo, &hi);
+            if (rc != RADAMW_OK) return rc;
+            if (hi != 0) {
+                if (end > hi) return RADAMW_ERR_INVALID;
+                extent_[extents_++] = {lo, hi, false};
+            }
+        }
+        range_[ranges_++] = {a, end, written};
+        return RADAMW_OK;
+    }
+
+    // RADAMW_ERR_ALIAS when a written range overlaps another one.
+    int alias() {
+        for (int i = 0; i < ranges_; ++i)
+            for (int j = i + 1; j < ranges_; ++j)
+                if ((range_[i].written || range_[j].written) && range_[i].lo < range_[j].hi &&
+                    range_[j].lo < range_[i].hi)
+                    return RADAMW_ERR_ALIAS;
+        return RADAMW_OK;
+    }
+
+  private:
+    static constexpr int MOST = 24;
+    int dev_;
+    int extents_ = 0, ranges_ = 0;
+    Range extent_[MOST], range_[MOST];
+};
+
+inline bool valid_index(int idt) { return idt == RADAMW_I32 || idt == RADAMW_I64; }
+inline size_t index_bytes(int idt) { return idt == RADAMW_I64 ? 8 : 4; }
+
+// Bytes a [n, width] array with row stride `stride` spans.
+inline int64_t span(int64_t n, int64_t width, int64_t stride, size_t elem) {
+    return n > 0 && width > 0 ? ((n - 1) * stride + width) * static_cast<int64_t>(elem) : 0;
+}
+
+// Counts, widths and strides that index without overflow.
+inline int check_rows(int64_t n, int64_t width, int64_t stride, int64_t max_width) {
+    if (n < 0 || width < 1 || stride < width) return RADAMW_ERR_INVALID;
+    if (n > MAX_ROWS || width > max_width || stride > MAX_ELEMENTS) return RADAMW_ERR_RANGE;
+    if (n > 0 && stride > MAX_ELEMENTS / n) return RADAMW_ERR_RANGE;
+    return RADAMW_OK;
+}
+
+inline void count_launches(int k) { g_launches.fetch_add(static_cast<uint64_t>(k), std::memory_order_relaxed); }
+
+inline int finite_scale(double s) {
+    return std::isfinite(s) && std::isfinite(static_cast<float>(s)) ? RADAMW_OK : RADAMW_ERR_INVALID;
 }
 
 }  // namespace radamw

@@ -9,8 +9,6 @@
 
 namespace radamw {
 
-// Largest row, token and vocabulary counts: they index with 31 bits.
-constexpr int64_t VOCAB_MAX_ROWS = 0x7ffffff0;
 // A launch addresses fewer than 2^32 work-items along x: workgroups of up to
 // 256 lanes.
 constexpr int64_t LAUNCH_MAX_BLOCKS = (int64_t(1) << 24) - 1;
