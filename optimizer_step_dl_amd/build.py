@@ -12,6 +12,8 @@ import argparse
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -23,23 +25,34 @@ SOURCES = ["radamw_api.cpp", "radamw_update.hip", "radamw_stats.hip", "radamw_st
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
-    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
+    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     "-Wall", "-Wno-unused-function",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-    "-x", "hip",
 ]
 
 
-def build(defines: list[str] | None = None, out: str | None = None, quiet: bool = True) -> str:
-    out = out or LIB_PATH
-    cmd = [HIPCC, *FLAGS, f"-I{INCLUDE}", f"-I{CSRC}", *[f"-D{d}" for d in (defines or [])],
-           *[os.path.join(CSRC, s) for s in SOURCES], "-o", out + ".tmp"]
+def _run(cmd: list[str], quiet: bool) -> None:
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
         raise RuntimeError(f"hipcc failed ({res.returncode}): {' '.join(cmd)}")
     if not quiet:
         sys.stderr.write(res.stderr)
+
+
+def build(defines: list[str] | None = None, out: str | None = None, quiet: bool = True) -> str:
+    """Compile the sources side by side, link them, and put the library in
+    place when it is whole."""
+    out = out or LIB_PATH
+    common = [f"-I{INCLUDE}", f"-I{CSRC}", *[f"-D{d}" for d in (defines or [])]]
+    with tempfile.TemporaryDirectory() as tmp:
+        objects = [os.path.join(tmp, s + ".o") for s in SOURCES]
+        with ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+            jobs = [pool.submit(_run, [HIPCC, *FLAGS, *common, "-x", "hip", "-c", os.path.join(CSRC, s), "-o", o], quiet)
+                    for s, o in zip(SOURCES, objects)]
+            for j in jobs:
+                j.result()
+        _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *objects, "-o", out + ".tmp"], quiet)
     os.replace(out + ".tmp", out)
     return out
 
