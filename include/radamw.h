@@ -760,6 +760,197 @@ int radamw_logits_grad(const void *logits, radamw_dtype dtype, int64_t n, int64_
                        const float *upstream, double grad_scale, void *grad, int64_t grad_stride,
                        radamw_stream_t stream);
 
+/*
+ * ------------------------------------------------------- block operators --
+ *
+ * Between the vocabulary's two ends: what a training step does around every
+ * block of a model.  Dropout from a counter-based generator (of the looked-up
+ * embedding, and inside the next operator); the residual stream's norms
+ * behind and before a block, fused with the block's dropout, gate and scale,
+ * and their gradient; the balance loss of a router with its per-expert counts
+ * and gradient.  The conventions are those of the vocabulary operators: row
+ * strides, index types, FP32 or FP64 sums in a fixed order, one rounding,
+ * streams, no capture, nothing kept.
+ */
+
+/*
+ * Dropout:
+ *   out[t, j] = kept ? x[t, j] * 65536 / (65536 - m) : 0,   m = round(65536 p)
+ * The probability is that of 16 bits, m / 65536 (halves round up); the factor
+ * is that probability's, in FP32.  The gradient is the same call on the
+ * output's gradient: the mask is formed again, not stored.
+ *
+ * An element's 16-bit number depends on seed, offset, its row and its column
+ * alone, and it is dropped where the number is below m: Philox 4x32 with ten
+ * rounds, the key {seed's low word, high word}, the counter {column / 8,
+ * first_row + row, offset's low word, high word}; column 8 q + 2 i + b has
+ * the half b (0: low) of output word i.  So a part of a batch (first_row), a
+ * strided view or a recomputed pass has the numbers of the whole, and calls
+ * that shall differ (layers, steps) have to differ in seed or offset.
+ * A dropped element is 0 whatever x holds there.
+ *   x, out  : [n, dim] of dtype; out may be exactly x (pointer and stride).
+ *   opts    : host; 0 <= p <= 1, first_row >= 0; first_row + n <= 2^32
+ *             (RADAMW_ERR_RANGE).  p = 1 gives zeros.
+ * dim <= 2^24.
+ */
+typedef struct {
+    double p;
+    uint64_t seed;
+    uint64_t offset;
+    int64_t first_row;
+} radamw_dropout_options;
+/* No dropout, all else 0. */
+radamw_dropout_options radamw_dropout_options_default(void);
+int radamw_dropout(const void *x, radamw_dtype dtype, int64_t n, int64_t dim, int64_t stride,
+                   const radamw_dropout_options *opts, void *out, int64_t out_stride, radamw_stream_t stream);
+
+/*
+ * The residual stream from one block's output to the next block's input:
+ *   u[t]   = post_weight ? norm(branch[t]) * (weight_offset + post_weight)
+ *                        : branch[t]
+ *   h[t]   = x[t] + residual_scale * gate[t / rows_per_gate] * drop(u[t])
+ *   out[t] = norm(h[t]) * (weight_offset + pre_weight)
+ *   norm(v) = v / sqrt(mean(v^2) + eps)
+ * all in FP32 from h's unrounded value; products are elementwise; drop is
+ * radamw_dropout's (opts->dropout, 0 for none).
+ *   branch : [n, dim] of branch_dtype, the block's output.  NULL: no block
+ *            before the norm; then h = x is not written (h, gate and
+ *            post_weight have to be NULL) and pre_weight is required.
+ *   gate   : [ceil(n / rows_per_gate), dim] of gate_dtype, or NULL: 1.  One
+ *            row for all rows (rows_per_gate >= n), one per sequence of equal
+ *            lengths, or one per row (rows_per_gate = 1).
+ *   post_weight, pre_weight : dim values of weight_dtype each, or NULL: no
+ *            such norm.  Without pre_weight there is no out (NULL).
+ *   x, h   : [n, dim] of stream_dtype, which is branch_dtype or RADAMW_F32.
+ *            h may be exactly x.
+ *   out    : [n, dim] of branch_dtype; may be exactly the branch.
+ *   rstd   : 2 n FP32, or NULL: 1 / sqrt(mean + eps) of the branch's rows
+ *            (written with a post_weight), then of h's (with a pre_weight),
+ *            for the gradient.
+ * dim <= 32768 (RADAMW_ERR_RANGE).  eps > 0, also as FP32.  A mean square
+ * beyond FP32 counts as infinite (values from about 1.8e19 / sqrt(dim) on).
+ */
+typedef struct {
+    int64_t n, dim;
+    radamw_dtype stream_dtype, branch_dtype, gate_dtype, weight_dtype;
+    const void *branch;
+    int64_t branch_stride;
+    const void *gate;
+    int64_t gate_stride;
+    int64_t rows_per_gate;
+    const void *post_weight;
+    const void *pre_weight;
+} radamw_residual_block;
+typedef struct {
+    double eps;
+    double weight_offset;
+    double residual_scale;
+    radamw_dropout_options dropout;
+} radamw_residual_options;
+/* eps 1e-6, weight_offset 0, residual_scale 1, no dropout. */
+radamw_residual_options radamw_residual_options_default(void);
+int radamw_residual_norm(const radamw_residual_block *block, const void *x, int64_t x_stride,
+                         const radamw_residual_options *opts, void *h, int64_t h_stride, void *out, int64_t out_stride,
+                         float *rstd, radamw_stream_t stream);
+
+/*
+ * The gradient of radamw_residual_norm, from grad_h (of h's later uses) and
+ * grad_out:
+ *   D           = grad_h + the gradient of out = norm(h) * (...) by h
+ *   grad_x      = D
+ *   grad_branch, grad_gate, grad_post_weight = those of
+ *                 residual_scale * gate * drop(u) under D
+ *   grad_pre_weight[j] = sum over rows of grad_out * norm(h)
+ * block and opts are the forward call's, h and rstd what it wrote (h unused
+ * without a pre_weight; where there was no branch, h is its x).
+ *   grad_h   : [n, dim] of stream_dtype, or NULL (zeros) with a pre_weight.
+ *   grad_out : [n, dim] of branch_dtype; exactly with a pre_weight.
+ *   grad_x   : [n, dim] of stream_dtype; may be exactly grad_h.
+ *   grad_branch : [n, dim] of branch_dtype, exactly with a branch; may be
+ *                 exactly grad_out.
+ *   grad_gate   : as the gate, of gate_dtype (all of its rows are written), or
+ *                 NULL.
+ *   grad_post_weight, grad_pre_weight : dim values of weight_dtype, or NULL.
+ *   workspace : device, 16-byte aligned, at least
+ *               radamw_residual_grad_workspace_bytes(n, dim, rows_per_gate)
+ *               (rows_per_gate 1 without a gate); in use until the stream has
+ *               passed the call.  May be NULL where no weight's gradient and
+ *               no shared gate's is asked for.
+ * Sums over rows are formed in FP32 by parts of the rows, which are joined in
+ * FP64, in an order that n and dim fix.  A dropped element passes nothing on,
+ * whatever the branch holds there.  With n = 0 the weights' gradients are
+ * zeros.
+ */
+int64_t radamw_residual_grad_workspace_bytes(int64_t n, int64_t dim, int64_t rows_per_gate);
+int radamw_residual_norm_grad(const radamw_residual_block *block, const void *h, int64_t h_stride, const float *rstd,
+                              const radamw_residual_options *opts, const void *grad_h, int64_t grad_h_stride,
+                              const void *grad_out, int64_t grad_out_stride, void *grad_x, int64_t grad_x_stride,
+                              void *grad_branch, int64_t grad_branch_stride, void *grad_gate, int64_t grad_gate_stride,
+                              void *grad_post_weight, void *grad_pre_weight, void *workspace, int64_t workspace_bytes,
+                              radamw_stream_t stream);
+
+/*
+ * Balance loss of a router over groups of token rows, with a z-loss and the
+ * per-expert counts.  Per group, over its T rows that take part:
+ *   P_te   = softmax of logits[t], or sigmoid(logits[t, e]) divided by the
+ *            row's sum of them (opts->score)
+ *   c_e    = how many of the rows' top_k ids are e
+ *   loss   = balance_coef * E / (top_k * T) * sum_e c_e * mean_t P_te
+ *            + z_coef * mean_t (log sum_e exp logits[t, e])^2
+ *   total  = sum of weights_g * loss_g
+ *   grad   = grad_scale * d total / d logits (the counts are constants)
+ * (balance_coef where every expert is chosen equally often.)
+ *   logits  : [n, experts] of dtype, row stride `stride`; experts <= 4096.
+ *   ids     : n * top_k indices, the experts each row chose; one outside
+ *             0 .. experts-1 is not counted, one given twice counts twice.
+ *   mask    : n bytes, or NULL: all 1.  A row of mask 0 takes no part: its
+ *             logits and ids may hold anything, its gradient is zeros.
+ *   offsets : groups + 1 indices of index_type, non-decreasing, within 0 ..
+ *             n: group g holds rows offsets[g] .. offsets[g + 1] - 1 (read on
+ *             the device; other values are clamped to 0 .. n for every
+ *             access, but the result is unspecified).  Rows outside every
+ *             group take no part.  NULL: one group (groups = 1) of all rows.
+ *   weights : groups FP32, or NULL: all 1.  A group of weight 0 adds nothing.
+ *   opts    : host; coefficients >= 0, finite; z_coef 0 with sigmoid scores.
+ *   total   : 1 FP32.  loss : groups FP32.
+ *   counts  : [groups, experts] int32.  tokens : groups int32 (T).
+ *   mean_prob : [groups, experts] FP32, mean_t P_te.
+ *   grad    : [n, experts] of dtype, or NULL; may be exactly the logits.
+ *   workspace : device, 16-byte aligned, at least
+ *               radamw_balance_workspace_bytes(n, experts, groups).
+ * A group without rows has loss 0.  A row whose logits are all -inf (or whose
+ * scores are all 0) adds no probability and has a zero gradient.
+ * n * top_k <= 2^31 - 16 and groups below 2^24 (RADAMW_ERR_RANGE).
+ *
+ * radamw_balance_grad is the gradient from the forward call's counts and
+ * tokens, for a backward pass that learns its scale (upstream, 1 FP32 on the
+ * device, or NULL: 1) only then.  counts and tokens may be sums over the
+ * ranks of a data-parallel job: the loss is then the whole batch's.
+ */
+typedef enum {
+    RADAMW_SCORE_SOFTMAX = 0,
+    RADAMW_SCORE_SIGMOID = 1
+} radamw_score_type;
+typedef struct {
+    double balance_coef;
+    double z_coef;
+    int32_t score; /* radamw_score_type */
+} radamw_balance_options;
+/* balance 0.01, no z-loss, softmax. */
+radamw_balance_options radamw_balance_options_default(void);
+int64_t radamw_balance_workspace_bytes(int64_t n, int64_t experts, int64_t groups);
+int radamw_balance_loss(const void *logits, radamw_dtype dtype, int64_t n, int64_t experts, int64_t stride,
+                        const void *ids, radamw_index_type index_type, int64_t top_k, const uint8_t *mask,
+                        const void *offsets, int64_t groups, const float *weights, const radamw_balance_options *opts,
+                        double grad_scale, float *total, float *loss, int32_t *counts, int32_t *tokens,
+                        float *mean_prob, void *grad, int64_t grad_stride, void *workspace, int64_t workspace_bytes,
+                        radamw_stream_t stream);
+int radamw_balance_grad(const void *logits, radamw_dtype dtype, int64_t n, int64_t experts, int64_t stride,
+                        int64_t top_k, const uint8_t *mask, const void *offsets, radamw_index_type offsets_type,
+                        int64_t groups, const float *weights, const radamw_balance_options *opts, const int32_t *counts,
+                        const int32_t *tokens, const float *upstream, double grad_scale, void *grad,
+                        int64_t grad_stride, radamw_stream_t stream);
+
 /* Utilities. */
 const char *radamw_status_string(int status);
 /* Last HIP error code seen by this thread inside the library (0 = none). */

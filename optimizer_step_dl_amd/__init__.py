@@ -5,9 +5,9 @@ ctypes binding whose functions carry the C entry points' names.
 Build in-tree first: ``python -m optimizer_step_dl_amd.build``.
 """
 from ._abi import (  # noqa: F401
-    AdamWState, Control, DecisionMismatch, FusedResult, Options, PolicyOptions, PreferenceOptions, RadamwError, Segment, SegmentList, Stats, TensorList, EXPORTS,
+    AdamWState, BalanceOptions, Control, DecisionMismatch, DropoutOptions, FusedResult, Options, PolicyOptions, PreferenceOptions, RadamwError, ResidualOptions, Segment, SegmentList, Stats, TensorList, EXPORTS,
     LIB_PATH,
-    bucket_arena, bucket_segment, control, load, options, policy_options, preference_options, radamw_bucket_layout,
+    balance_options, bucket_arena, bucket_segment, control, dropout_options, load, options, policy_options, preference_options, residual_options, radamw_bucket_layout,
     radamw_check_decision, radamw_decide, radamw_fused_step_multi, radamw_fused_step_multi_noalloc, radamw_fused_workspace_bytes, radamw_grad_stats,
     radamw_grad_stats_rows, radamw_host_coefficients, radamw_last_hip_error, radamw_launch_count,
     radamw_list_create, radamw_list_destroy, radamw_list_fused_step, radamw_list_step, radamw_lists_fused_step,
@@ -17,4 +17,7 @@ from ._abi import (  # noqa: F401
     radamw_time_next_update, radamw_embedding_lookup, radamw_embedding_grad, radamw_embedding_grad_workspace_bytes,
     radamw_policy_loss, radamw_policy_options_default, radamw_preference_loss, radamw_preference_options_default,
     radamw_logits_grad,
+    radamw_balance_grad, radamw_balance_loss, radamw_balance_options_default, radamw_balance_workspace_bytes,
+    radamw_dropout, radamw_dropout_options_default, radamw_residual_grad_workspace_bytes, radamw_residual_norm,
+    radamw_residual_norm_grad, radamw_residual_options_default,
 )

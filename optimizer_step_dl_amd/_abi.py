@@ -85,6 +85,28 @@ class PreferenceOptions(ctypes.Structure):
     _fields_ = [("beta", ctypes.c_double), ("label_smoothing", ctypes.c_double)]
 
 
+class DropoutOptions(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64),
+                ("first_row", ctypes.c_int64)]
+
+
+class ResidualOptions(ctypes.Structure):
+    _fields_ = [("eps", ctypes.c_double), ("weight_offset", ctypes.c_double), ("residual_scale", ctypes.c_double),
+                ("dropout", DropoutOptions)]
+
+
+class _ResidualBlock(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("dim", ctypes.c_int64), ("stream_dtype", ctypes.c_int32),
+                ("branch_dtype", ctypes.c_int32), ("gate_dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32),
+                ("branch", ctypes.c_void_p), ("branch_stride", ctypes.c_int64), ("gate", ctypes.c_void_p),
+                ("gate_stride", ctypes.c_int64), ("rows_per_gate", ctypes.c_int64), ("post_weight", ctypes.c_void_p),
+                ("pre_weight", ctypes.c_void_p)]
+
+
+class BalanceOptions(ctypes.Structure):
+    _fields_ = [("balance_coef", ctypes.c_double), ("z_coef", ctypes.c_double), ("score", ctypes.c_int32)]
+
+
 class Stats(ctypes.Structure):
     _fields_ = [("w", ctypes.c_uint32 * 3)]
 
@@ -116,6 +138,31 @@ def policy_options(clip_low=0.2, clip_high=0.2, kl_coef=0.0) -> PolicyOptions:
 
 def preference_options(beta=0.1, label_smoothing=0.0) -> PreferenceOptions:
     return PreferenceOptions(float(beta), float(label_smoothing))
+
+
+def _word64(v: int, what: str) -> int:
+    if not 0 <= int(v) < 1 << 64:
+        raise ValueError(f"{what} must be within 0 .. 2^64 - 1 (got {v})")
+    return int(v)
+
+
+def dropout_options(p=0.0, seed=0, offset=0, first_row=0) -> DropoutOptions:
+    return DropoutOptions(float(p), _word64(seed, "seed"), _word64(offset, "offset"), int(first_row))
+
+
+def residual_options(eps=1e-6, weight_offset=0.0, residual_scale=1.0, p=0.0, seed=0, offset=0,
+                     first_row=0) -> ResidualOptions:
+    return ResidualOptions(float(eps), float(weight_offset), float(residual_scale),
+                           dropout_options(p, seed, offset, first_row))
+
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def balance_options(balance_coef=0.01, z_coef=0.0, score="softmax") -> BalanceOptions:
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)} (got {score!r})")
+    return BalanceOptions(float(balance_coef), float(z_coef), _SCORES[score])
 
 
 def control(gradient_scale=1.0, skip_update=False) -> Control:
@@ -206,6 +253,20 @@ def load(path: str = LIB_PATH):
         "radamw_preference_loss": ([vp, i32, i64, i64, i64, vp, i32, vp, i64, vp, vp, P(PreferenceOptions), dbl, vp, vp,
                                     vp, vp, vp, vp, i64, vp], ctypes.c_int),
         "radamw_logits_grad": ([vp, i32, i64, i64, i64, vp, i32, vp, vp, dbl, vp, i64, vp], ctypes.c_int),
+        "radamw_dropout_options_default": ([], DropoutOptions),
+        "radamw_dropout": ([vp, i32, i64, i64, i64, P(DropoutOptions), vp, i64, vp], ctypes.c_int),
+        "radamw_residual_options_default": ([], ResidualOptions),
+        "radamw_residual_norm": ([P(_ResidualBlock), vp, i64, P(ResidualOptions), vp, i64, vp, i64, vp, vp],
+                                 ctypes.c_int),
+        "radamw_residual_grad_workspace_bytes": ([i64, i64, i64], i64),
+        "radamw_residual_norm_grad": ([P(_ResidualBlock), vp, i64, vp, P(ResidualOptions), vp, i64, vp, i64, vp, i64, vp,
+                                       i64, vp, i64, vp, vp, vp, i64, vp], ctypes.c_int),
+        "radamw_balance_options_default": ([], BalanceOptions),
+        "radamw_balance_workspace_bytes": ([i64, i64, i64], i64),
+        "radamw_balance_loss": ([vp, i32, i64, i64, i64, vp, i32, i64, vp, vp, i64, vp, P(BalanceOptions), dbl, vp, vp,
+                                 vp, vp, vp, vp, i64, vp, i64, vp], ctypes.c_int),
+        "radamw_balance_grad": ([vp, i32, i64, i64, i64, i64, vp, vp, i32, i64, vp, P(BalanceOptions), vp, vp, vp, dbl,
+                                 vp, i64, vp], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -224,7 +285,10 @@ EXPORTS = ("radamw_options_default", "radamw_step", "radamw_step_inplace", "rada
            "radamw_list_create", "radamw_list_step", "radamw_list_fused_step", "radamw_list_destroy",
            "radamw_lists_fused_step", "radamw_embedding_lookup", "radamw_embedding_grad_workspace_bytes",
            "radamw_embedding_grad", "radamw_policy_options_default", "radamw_policy_loss",
-           "radamw_preference_options_default", "radamw_preference_loss", "radamw_logits_grad")
+           "radamw_preference_options_default", "radamw_preference_loss", "radamw_logits_grad",
+           "radamw_dropout_options_default", "radamw_dropout", "radamw_residual_options_default", "radamw_residual_norm",
+           "radamw_residual_grad_workspace_bytes", "radamw_residual_norm_grad", "radamw_balance_options_default",
+           "radamw_balance_workspace_bytes", "radamw_balance_loss", "radamw_balance_grad")
 
 
 # ----------------------------------------------------------------- helpers --
@@ -979,6 +1043,254 @@ def radamw_logits_grad(logits: torch.Tensor, labels: torch.Tensor, row_stats: to
     ups = _row_values(upstream, "upstream", 1, dev.index)
     _submit("radamw_logits_grad", lib.radamw_logits_grad, dev, logits.data_ptr(), _DTYPE_CODE[logits.dtype], n, vocab,
             st, labels.data_ptr(), idt, sta, ups, float(grad_scale), gp, gs)
+
+
+# ----------------------------------------------------------- block operators --
+
+def radamw_dropout_options_default() -> DropoutOptions:
+    return load().radamw_dropout_options_default()
+
+
+def radamw_residual_options_default() -> ResidualOptions:
+    return load().radamw_residual_options_default()
+
+
+def radamw_balance_options_default() -> BalanceOptions:
+    return load().radamw_balance_options_default()
+
+
+def radamw_dropout(x: torch.Tensor, out: torch.Tensor, opts: DropoutOptions) -> None:
+    """out = x / keep where the generator keeps an element, else 0, for x and
+    out [n, dim] of one dtype (out may be x)."""
+    lib = load()
+    dev = x.device
+    xs = _rows2d(x, "x", dev)
+    n, dim = x.shape
+    os_ = _rows2d(out, "out", dev, n, dim)
+    if out.dtype != x.dtype:
+        raise ValueError(f"out must be {x.dtype} (got {out.dtype})")
+    _submit("radamw_dropout", lib.radamw_dropout, dev, x.data_ptr(), _DTYPE_CODE[x.dtype], n, dim, xs,
+            ctypes.byref(opts), out.data_ptr(), os_)
+
+
+def _typed_rows(t: Optional[torch.Tensor], what: str, device, n: int, dim: int, dtype: torch.dtype):
+    """(pointer, row stride) of an optional [n, dim] tensor of a dtype."""
+    if t is None:
+        return None, 0
+    stride = _rows2d(t, what, device, n, dim)
+    if t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype} (got {t.dtype})")
+    return t.data_ptr(), stride
+
+
+def _column_values(t: Optional[torch.Tensor], what: str, dim: int, dev_index: int, dtype: torch.dtype):
+    """Pointer of an optional contiguous [dim] tensor of a dtype."""
+    if t is None:
+        return None
+    try:
+        good = t.dtype is dtype and t.numel() == dim and t.get_device() == dev_index and t.is_contiguous()
+    except AttributeError:
+        good = False
+    if not good:
+        _check_fast(t, what, dev_index, dim, dtype)  # says what is wrong
+    return t.data_ptr()
+
+
+def _residual_block(like: torch.Tensor, stream_dtype, branch_dtype, branch, gate, rows_per_gate, post_weight,
+                    pre_weight) -> _ResidualBlock:
+    """The shapes and inputs that both residual calls share; ``like`` has the
+    stream's shape and device."""
+    dev = like.device
+    n, dim = like.shape
+    b = _ResidualBlock(n=n, dim=dim, stream_dtype=_DTYPE_CODE[stream_dtype], branch_dtype=_DTYPE_CODE[branch_dtype],
+                       rows_per_gate=1)
+    if branch is not None:
+        b.branch, b.branch_stride = branch.data_ptr(), _rows2d(branch, "branch", dev, n, dim)
+    if gate is not None:
+        if rows_per_gate is None:  # one gate row for equal numbers of rows
+            rows_per_gate = -(-n // max(1, gate.shape[0])) or 1
+        b.rows_per_gate = int(rows_per_gate)
+        if b.rows_per_gate < 1:
+            raise ValueError(f"rows_per_gate must be at least 1 (got {rows_per_gate})")
+        b.gate_stride = _rows2d(gate, "gate", dev, -(-n // b.rows_per_gate), dim)
+        b.gate, b.gate_dtype = gate.data_ptr(), _DTYPE_CODE[gate.dtype]
+    weight = post_weight if post_weight is not None else pre_weight
+    if weight is not None:
+        if weight.dtype not in _DTYPE_CODE:
+            raise ValueError(f"weight dtype {weight.dtype} is not float32/float16/bfloat16")
+        b.weight_dtype = _DTYPE_CODE[weight.dtype]
+        b.post_weight = _column_values(post_weight, "post_weight", dim, dev.index, weight.dtype)
+        b.pre_weight = _column_values(pre_weight, "pre_weight", dim, dev.index, weight.dtype)
+    return b
+
+
+def radamw_residual_norm(x: torch.Tensor, branch: Optional[torch.Tensor], opts: ResidualOptions, *,
+                         gate: Optional[torch.Tensor] = None, rows_per_gate: Optional[int] = None,
+                         post_weight: Optional[torch.Tensor] = None, pre_weight: Optional[torch.Tensor] = None,
+                         h: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                         rstd: Optional[torch.Tensor] = None) -> None:
+    """h = x + residual_scale * gate * drop(norm(branch) * post_weight) and out
+    = norm(h) * pre_weight, for x, branch, h, out [n, dim], gate [ceil(n /
+    rows_per_gate), dim], weights [dim] and rstd (2 n FP32, the norms' records
+    for the gradient).  Absent: no gate, no such norm; without a branch only
+    out is written.  h may be x, out may be the branch."""
+    lib = load()
+    dev = x.device
+    xs = _rows2d(x, "x", dev)
+    n, dim = x.shape
+    kind = branch if branch is not None else out if out is not None else x
+    if not isinstance(kind, torch.Tensor) or kind.dtype not in _DTYPE_CODE:
+        raise ValueError("branch and out must be float32/float16/bfloat16 device tensors")
+    b = _residual_block(x, x.dtype, kind.dtype, branch, gate, rows_per_gate, post_weight, pre_weight)
+    hp, hs = _typed_rows(h, "h", dev, n, dim, x.dtype)
+    op, os_ = _typed_rows(out, "out", dev, n, dim, kind.dtype)
+    rp = _row_values(rstd, "rstd", 2 * n, dev.index)
+    _submit("radamw_residual_norm", lib.radamw_residual_norm, dev, ctypes.byref(b), x.data_ptr(), xs,
+            ctypes.byref(opts), hp, hs, op, os_, rp)
+
+
+def radamw_residual_grad_workspace_bytes(n: int, dim: int, rows_per_gate: int = 1) -> int:
+    r = load().radamw_residual_grad_workspace_bytes(n, dim, rows_per_gate)
+    if r < 0:
+        raise RadamwError(int(r), "radamw_residual_grad_workspace_bytes")
+    return int(r)
+
+
+def radamw_residual_norm_grad(h: Optional[torch.Tensor], branch: Optional[torch.Tensor], opts: ResidualOptions,
+                              rstd: Optional[torch.Tensor], workspace: Optional[torch.Tensor], *,
+                              grad_x: torch.Tensor, gate: Optional[torch.Tensor] = None,
+                              rows_per_gate: Optional[int] = None, post_weight: Optional[torch.Tensor] = None,
+                              pre_weight: Optional[torch.Tensor] = None, grad_h: Optional[torch.Tensor] = None,
+                              grad_out: Optional[torch.Tensor] = None, grad_branch: Optional[torch.Tensor] = None,
+                              grad_gate: Optional[torch.Tensor] = None,
+                              grad_post_weight: Optional[torch.Tensor] = None,
+                              grad_pre_weight: Optional[torch.Tensor] = None) -> None:
+    """The gradients of radamw_residual_norm from grad_h and grad_out: grad_x
+    and grad_branch [n, dim] (which may be grad_h and grad_out), and those
+    asked for of grad_gate, grad_post_weight and grad_pre_weight.
+    ``workspace`` holds at least radamw_residual_grad_workspace_bytes(n, dim,
+    rows_per_gate) bytes (None where no weight's or shared gate's gradient is
+    asked for)."""
+    lib = load()
+    dev = grad_x.device
+    gxs = _rows2d(grad_x, "grad_x", dev)
+    n, dim = grad_x.shape
+    kind = branch if branch is not None else grad_out if grad_out is not None else grad_x
+    if not isinstance(kind, torch.Tensor) or kind.dtype not in _DTYPE_CODE:
+        raise ValueError("branch and grad_out must be float32/float16/bfloat16 device tensors")
+    b = _residual_block(grad_x, grad_x.dtype, kind.dtype, branch, gate, rows_per_gate, post_weight, pre_weight)
+    hp, hs = _typed_rows(h if pre_weight is not None else None, "h", dev, n, dim, grad_x.dtype)
+    rp = _row_values(rstd, "rstd", 2 * n, dev.index)
+    ghp, ghs = _typed_rows(grad_h, "grad_h", dev, n, dim, grad_x.dtype)
+    gop, gos = _typed_rows(grad_out, "grad_out", dev, n, dim, kind.dtype)
+    gbp, gbs = _typed_rows(grad_branch, "grad_branch", dev, n, dim, kind.dtype)
+    ggp, ggs = (None, 0) if grad_gate is None or gate is None else _typed_rows(grad_gate, "grad_gate", dev,
+                                                                              gate.shape[0], dim, gate.dtype)
+    if grad_gate is not None and gate is None:
+        raise ValueError("grad_gate without a gate")
+    for g, w, what in ((grad_post_weight, post_weight, "post_weight"), (grad_pre_weight, pre_weight, "pre_weight")):
+        if g is not None and w is None:
+            raise ValueError(f"grad_{what} without a {what}")
+    gpost = None if post_weight is None else _column_values(grad_post_weight, "grad_post_weight", dim, dev.index,
+                                                            post_weight.dtype)
+    gpre = None if pre_weight is None else _column_values(grad_pre_weight, "grad_pre_weight", dim, dev.index,
+                                                          pre_weight.dtype)
+    if workspace is not None:
+        _dense(workspace, "workspace", device=dev)
+    _submit("radamw_residual_norm_grad", lib.radamw_residual_norm_grad, dev, ctypes.byref(b), hp, hs, rp,
+            ctypes.byref(opts), ghp, ghs, gop, gos, grad_x.data_ptr(), gxs, gbp, gbs, ggp, ggs, gpost, gpre,
+            _ptr_or_none(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size())
+
+
+def _whole(t: torch.Tensor, what: str, n: int, dev_index: int, dtype: torch.dtype):
+    """Pointer of a contiguous tensor of n values of a dtype."""
+    return _column_values(t, what, n, dev_index, dtype)
+
+
+def _balance_inputs(logits, offsets, mask, weights, groups, index_code):
+    """Checked pointers of offsets, mask and weights, and the index type."""
+    dev = logits.device
+    n = logits.shape[0]
+    off = None
+    if offsets is not None:
+        code = _index(offsets, "offsets", groups + 1, dev)
+        if index_code is not None and code != index_code:
+            raise ValueError(f"offsets must have the ids' type (got {offsets.dtype})")
+        index_code, off = code, offsets.data_ptr()
+    elif groups != 1:
+        raise ValueError(f"{groups} groups need offsets")
+    msk = None
+    if mask is not None:
+        if getattr(mask, "dtype", None) not in (torch.bool, torch.uint8):
+            raise ValueError("mask must be a bool or uint8 tensor")
+        msk = _whole(mask, "mask", n, dev.index, mask.dtype)
+    return off, msk, _row_values(weights, "weights", groups, dev.index), index_code or 0
+
+
+def radamw_balance_workspace_bytes(n: int, experts: int, groups: int = 1) -> int:
+    r = load().radamw_balance_workspace_bytes(n, experts, groups)
+    if r < 0:
+        raise RadamwError(int(r), "radamw_balance_workspace_bytes")
+    return int(r)
+
+
+def radamw_balance_loss(logits: torch.Tensor, ids: torch.Tensor, opts: BalanceOptions, total: torch.Tensor,
+                        loss: torch.Tensor, counts: torch.Tensor, tokens: torch.Tensor, mean_prob: torch.Tensor,
+                        workspace: torch.Tensor, *, mask: Optional[torch.Tensor] = None,
+                        offsets: Optional[torch.Tensor] = None, weights: Optional[torch.Tensor] = None,
+                        grad: Optional[torch.Tensor] = None, grad_scale: float = 1.0) -> None:
+    """Balance loss of a router's logits [n, experts] with the experts ids [n,
+    top_k] that were chosen: writes total (1), loss (groups), counts [groups,
+    experts] and tokens (groups) (int32), mean_prob [groups, experts] and, when
+    ``grad`` is given, grad_scale * d total / d logits (``grad`` may be
+    ``logits``).  ``offsets`` (groups + 1, of the ids' type) give the rows of
+    each group; without them all rows are one group."""
+    lib = load()
+    dev = logits.device
+    st = _rows2d(logits, "logits", dev)
+    n, experts = logits.shape
+    di = dev.index
+    if ids.dim() != 2 or ids.shape[0] != n:
+        raise ValueError(f"ids must be [{n}, top_k] (got {tuple(ids.shape)})")
+    top_k = ids.shape[1]
+    idt = _index(ids, "ids", n * top_k, dev)
+    groups = loss.numel()
+    off, msk, wts, _ = _balance_inputs(logits, offsets, mask, weights, groups, idt)
+    tot = _row_values(total, "total", 1, di)
+    los = _row_values(loss, "loss", groups, di)
+    cnt = _whole(counts, "counts", groups * experts, di, torch.int32)
+    tok = _whole(tokens, "tokens", groups, di, torch.int32)
+    mpr = _row_values(mean_prob, "mean_prob", groups * experts, di)
+    gp, gs = _typed_rows(grad, "grad", dev, n, experts, logits.dtype)
+    _dense(workspace, "workspace", device=dev)
+    _submit("radamw_balance_loss", lib.radamw_balance_loss, dev, logits.data_ptr(), _DTYPE_CODE[logits.dtype], n,
+            experts, st, ids.data_ptr(), idt, top_k, msk, off, groups, wts, ctypes.byref(opts), float(grad_scale), tot,
+            los, cnt, tok, mpr, gp, gs, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+
+
+def radamw_balance_grad(logits: torch.Tensor, top_k: int, opts: BalanceOptions, counts: torch.Tensor,
+                        tokens: torch.Tensor, grad: torch.Tensor, *, mask: Optional[torch.Tensor] = None,
+                        offsets: Optional[torch.Tensor] = None, weights: Optional[torch.Tensor] = None,
+                        upstream: Optional[torch.Tensor] = None, grad_scale: float = 1.0) -> None:
+    """grad = upstream * grad_scale * d total / d logits from the counts and
+    tokens that radamw_balance_loss left; upstream is one FP32 value on the
+    device."""
+    lib = load()
+    dev = logits.device
+    st = _rows2d(logits, "logits", dev)
+    n, experts = logits.shape
+    di = dev.index
+    groups = tokens.numel()
+    off, msk, wts, idt = _balance_inputs(logits, offsets, mask, weights, groups, None)
+    cnt = _whole(counts, "counts", groups * experts, di, torch.int32)
+    tok = _whole(tokens, "tokens", groups, di, torch.int32)
+    ups = _row_values(upstream, "upstream", 1, di)
+    if grad is None:
+        raise ValueError("grad must be a device tensor")
+    gp, gs = _typed_rows(grad, "grad", dev, n, experts, logits.dtype)
+    _submit("radamw_balance_grad", lib.radamw_balance_grad, dev, logits.data_ptr(), _DTYPE_CODE[logits.dtype], n,
+            experts, st, int(top_k), msk, off, idt, groups, wts, ctypes.byref(opts), cnt, tok, ups, float(grad_scale),
+            gp, gs)
 
 
 def radamw_host_coefficients(opts: Options, t: int, gradient_scale: float = 1.0) -> list[float]:

@@ -148,6 +148,44 @@ __device__ __forceinline__ void stream8(void *p, int64_t e, f32x8 v) {
     }
 }
 
+// Eight values at column e < dim of a row; columns from dim on read as zeros
+// and are not stored.  TAIL: dim may be no multiple of eight.  SHARED: other
+// workgroups read the data as well, so that it is loaded without the
+// nontemporal hint.
+template <int DT, bool TAIL, bool SHARED = false>
+__device__ __forceinline__ Raw8<DT> load_piece(const void *row, int32_t e, int32_t dim) {
+    if (!TAIL || e + 8 <= dim) return SHARED ? load_raw8<DT>(row, e) : stream_raw8<DT>(row, e);
+    uint32_t b[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) b[j] = e + j < dim ? load_bits<DT>(row, e + j) : 0u;
+    Raw8<DT> r;
+    if constexpr (DT == G_F32) {
+        r.c[0] = u32x4{b[0], b[1], b[2], b[3]};
+        r.c[1] = u32x4{b[4], b[5], b[6], b[7]};
+    } else {
+        r.c[0] = u32x4{b[0] | b[1] << 16, b[2] | b[3] << 16, b[4] | b[5] << 16, b[6] | b[7] << 16};
+    }
+    return r;
+}
+template <int DT, bool TAIL>
+__device__ __forceinline__ void store_piece(void *row, int32_t e, int32_t dim, f32x8 v) {
+    if (!TAIL || e + 8 <= dim) {
+        stream8<DT>(row, e, v);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (e + j < dim) store_value<DT>(row, e + j, v[j]);
+}
+
+// Element `e` of an array whose elements' type is known at run time.
+__device__ __forceinline__ const char *elem_at(const void *p, int32_t dt, int64_t e) {
+    return static_cast<const char *>(p) + (dt == G_F32 ? e * 4 : e * 2);
+}
+__device__ __forceinline__ char *elem_at(void *p, int32_t dt, int64_t e) {
+    return static_cast<char *>(p) + (dt == G_F32 ? e * 4 : e * 2);
+}
+
 // Entry i of an index array, as 64 bits.
 __device__ __forceinline__ int64_t load_index(const void *p, int32_t wide, int64_t i) {
     return wide ? gl(static_cast<const int64_t *>(p))[i] : int64_t(gl(static_cast<const int32_t *>(p))[i]);

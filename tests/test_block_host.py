@@ -1,0 +1,266 @@
+"""CPU tests of the block operators: the C entry points' refusals that need no
+device, the binding's argument checks, workspace sizes, the generator against
+its authors' published vectors, and the plain 64-bit forms of block_helpers.py
+against torch's autograd and against differences."""
+import ctypes
+import math
+import os
+
+import pytest
+import torch
+
+import optimizer_step_dl_amd as ra
+from optimizer_step_dl_amd import _abi
+from block_helpers import DOUBLE, Residual, balance, dropout, keep_factor, keep_mask, philox
+
+INVALID, RANGE = -1, -5
+P = 0x10000  # a pointer that no refused call may look at
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(ra.LIB_PATH):
+        from optimizer_step_dl_amd import build
+        build.build()
+    return ra.load()
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+# --------------------------------------------------------------- refusals --
+
+def drop(lib, dt=0, n=3, dim=8, st=8, p=0.1, first=0, os_=8, opts=True):
+    o = ctypes.byref(_abi.DropoutOptions(p, 1, 2, first)) if opts else None
+    return lib.radamw_dropout(P, dt, n, dim, st, o, P, os_, None)
+
+
+def test_dropout_refusals(lib):
+    for kw in (dict(dt=3), dict(n=-1), dict(dim=0), dict(st=7), dict(os_=7), dict(p=-0.01), dict(p=1.01), dict(p=NAN),
+               dict(first=-1), dict(opts=False)):
+        assert drop(lib, **kw) == INVALID, kw
+    for kw in (dict(n=2 ** 31), dict(dim=2 ** 24 + 1, st=2 ** 25, os_=2 ** 25), dict(first=2 ** 32 - 2),
+               dict(st=2 ** 47, n=1000)):
+        assert drop(lib, **kw) == RANGE, kw
+    assert drop(lib, n=0) == 0 and drop(lib, n=0, first=2 ** 32) == 0
+
+
+def block(n=3, dim=8, sdt=0, bdt=0, gdt=0, wdt=0, branch=P, bs=8, gate=None, gs=8, per=1, post=P, pre=P):
+    return _abi._ResidualBlock(n, dim, sdt, bdt, gdt, wdt, branch, bs, gate, gs, per, post, pre)
+
+
+def norm(lib, k, eps=1e-6, off=0.0, scale=1.0, p=0.0, first=0, xs=8, h=P, hs=8, out=P, os_=8):
+    o = _abi.ResidualOptions(eps, off, scale, _abi.DropoutOptions(p, 0, 0, first))
+    return lib.radamw_residual_norm(ctypes.byref(k), P, xs, ctypes.byref(o), h, hs, out, os_, None, None)
+
+
+def norm_grad(lib, k, eps=1e-6, hs=8, gh=P, ghs=8, go=P, gos=8, gxs=8, gb=P, gbs=8, gg=None, ggs=8, gpost=P, gpre=P,
+              ws=1 << 40):
+    o = _abi.ResidualOptions(eps, 0.0, 1.0, _abi.DropoutOptions(0.0, 0, 0, 0))
+    return lib.radamw_residual_norm_grad(ctypes.byref(k), P, hs, P, ctypes.byref(o), gh, ghs, go, gos, P, gxs, gb, gbs,
+                                         gg, ggs, gpost, gpre, P, ws, None)
+
+
+SHARED = [dict(sdt=3), dict(bdt=-1), dict(sdt=1, bdt=2), dict(sdt=2, bdt=0), dict(wdt=5), dict(n=-1), dict(dim=0),
+          dict(bs=7), dict(gate=P, gdt=4), dict(gate=P, per=0), dict(gate=P, gs=7),
+          dict(branch=None), dict(branch=None, post=None, gate=P), dict(branch=None, post=None, pre=None)]
+
+
+def test_residual_refusals(lib):
+    for kw in SHARED:
+        assert norm(lib, block(**kw)) == INVALID, kw
+        assert norm_grad(lib, block(**kw)) == INVALID, kw
+    for kw in (dict(eps=0.0), dict(eps=-1.0), dict(eps=NAN), dict(eps=INF), dict(eps=1e-60), dict(off=INF),
+               dict(scale=1e39), dict(scale=NAN), dict(p=1.5), dict(first=-1), dict(xs=7), dict(hs=7), dict(os_=7)):
+        assert norm(lib, block(), **kw) == INVALID, kw
+    assert norm(lib, block(branch=None, post=None)) == INVALID  # h without a branch
+    assert norm(lib, block(pre=None)) == INVALID  # out without its norm
+    assert lib.radamw_residual_norm(None, P, 8, ctypes.byref(ra.residual_options()), P, 8, P, 8, None, None) == INVALID
+    assert lib.radamw_residual_norm(ctypes.byref(block()), P, 8, None, P, 8, P, 8, None, None) == INVALID
+    for kw in (dict(dim=32769, bs=40000), dict(n=2 ** 31), dict(bs=2 ** 47, n=1000)):
+        big = dict(xs=40000, hs=40000, os_=40000)
+        assert norm(lib, block(**kw), **big) == RANGE, kw
+    assert norm(lib, block(), first=2 ** 32 - 2) == RANGE
+    assert norm(lib, block(n=0)) == 0
+
+
+def test_residual_grad_refusals(lib):
+    for kw in (dict(eps=0.0), dict(hs=7), dict(ghs=7), dict(gos=7), dict(gxs=7), dict(gbs=7)):
+        assert norm_grad(lib, block(), **kw) == INVALID, kw
+    assert norm_grad(lib, block(gate=P), gg=P, ggs=7) == INVALID
+    assert norm_grad(lib, block(), gg=P) == INVALID  # a gradient of no gate
+    assert norm_grad(lib, block(post=None)) == INVALID  # of no weight
+    assert norm_grad(lib, block(branch=None, post=None), gpost=None) == INVALID  # of no branch
+    assert norm_grad(lib, block(pre=None)) == INVALID
+    assert norm_grad(lib, block(pre=None), gpre=None) == INVALID  # grad_out without its norm
+    assert norm_grad(lib, block(pre=None), gpre=None, go=None, gh=None) == INVALID  # no gradient at all
+    need = ra.radamw_residual_grad_workspace_bytes(3, 8)
+    assert norm_grad(lib, block(), ws=need - 1) == RANGE
+    assert norm_grad(lib, block(n=2 ** 31 - 1)) == RANGE
+    assert norm_grad(lib, block(n=0), gpost=None, gpre=None) == 0
+
+
+def loss(lib, dt=0, n=3, experts=8, st=8, idt=1, k=2, off=None, groups=1, coef=0.01, z=0.0, score=0, scale=1.0, grad=P,
+         gs=8, ws=1 << 40, opts=True):
+    o = ctypes.byref(_abi.BalanceOptions(coef, z, score)) if opts else None
+    return lib.radamw_balance_loss(P, dt, n, experts, st, P, idt, k, None, off, groups, None, o, scale, P, P, P, P, P,
+                                   grad, gs, P, ws, None)
+
+
+def loss_grad(lib, dt=0, n=3, experts=8, st=8, idt=1, k=2, off=None, groups=1, coef=0.01, z=0.0, score=0, scale=1.0,
+              gs=8, opts=True):
+    o = ctypes.byref(_abi.BalanceOptions(coef, z, score)) if opts else None
+    return lib.radamw_balance_grad(P, dt, n, experts, st, k, None, off, idt, groups, None, o, P, P, None, scale, P, gs,
+                                   None)
+
+
+def test_balance_refusals(lib):
+    for call in (loss, loss_grad):
+        for kw in (dict(dt=3), dict(idt=2), dict(n=-1), dict(experts=0), dict(st=7), dict(gs=7), dict(k=0),
+                   dict(groups=0), dict(groups=2), dict(coef=-1.0), dict(coef=NAN), dict(z=-1.0), dict(z=INF),
+                   dict(score=2), dict(score=1, z=0.1), dict(scale=INF), dict(opts=False)):
+            assert call(lib, **kw) == INVALID, kw
+        for kw in (dict(n=2 ** 31), dict(experts=4097, st=5000, gs=5000), dict(n=2 ** 30, k=3),
+                   dict(off=P, groups=2 ** 24), dict(st=2 ** 47, n=1000)):
+            assert call(lib, **kw) == RANGE, kw
+    assert loss(lib, ws=ra.radamw_balance_workspace_bytes(3, 8) - 1) == RANGE
+    assert loss_grad(lib, n=0) == 0
+
+
+def test_workspace_bytes(lib):
+    for n in (0, 1, 255, 4096, 100_000):
+        # four sums of a worker's columns, at most 1024 workers
+        b = ra.radamw_residual_grad_workspace_bytes(n, 4096)
+        assert 0 < b <= 4 * 4 * 4096 * max(1, min(n, 1024))
+        # sums and counts per piece, at most 1024 pieces and one per group
+        b = ra.radamw_balance_workspace_bytes(n, 256, 7)
+        assert 0 < b <= (1024 + 7) * (2 * 256 * 4 + 16) + 1024
+    for bad in ((-1, 8, 1), (3, 0, 1), (3, 8, 0), (2 ** 31, 8, 1), (3, 32769, 1)):
+        with pytest.raises(ra.RadamwError) as e:
+            ra.radamw_residual_grad_workspace_bytes(*bad)
+        assert e.value.status in (INVALID, RANGE)
+    for bad in ((-1, 8, 1), (3, 0, 1), (3, 8, 0), (2 ** 31, 8, 1), (3, 4097, 1), (3, 8, 2 ** 24)):
+        with pytest.raises(ra.RadamwError) as e:
+            ra.radamw_balance_workspace_bytes(*bad)
+        assert e.value.status in (INVALID, RANGE)
+
+
+def test_option_defaults(lib):
+    for d, e in ((ra.radamw_dropout_options_default(), ra.dropout_options()),
+                 (ra.radamw_balance_options_default(), ra.balance_options())):
+        assert [getattr(d, f) for f, _ in d._fields_] == [getattr(e, f) for f, _ in e._fields_]
+    d, e = ra.radamw_residual_options_default(), ra.residual_options()
+    assert (d.eps, d.weight_offset, d.residual_scale, d.dropout.p) == (1e-6, 0.0, 1.0, 0.0)
+    assert (e.eps, e.weight_offset, e.residual_scale, e.dropout.p) == (1e-6, 0.0, 1.0, 0.0)
+    for kw in (dict(seed=-1), dict(seed=2 ** 64), dict(offset=-1)):
+        with pytest.raises(ValueError):
+            ra.dropout_options(0.1, **kw)
+    with pytest.raises(ValueError):
+        ra.balance_options(score="tanh")
+
+
+def test_binding_refuses_host_tensors(lib):
+    x, ids, w = torch.zeros(4, 8), torch.zeros((4, 2), dtype=torch.int64), torch.zeros(8)
+    with pytest.raises(ValueError):
+        ra.radamw_dropout(x, x, ra.dropout_options(0.1))
+    with pytest.raises(ValueError):
+        ra.radamw_residual_norm(x, x, ra.residual_options(), pre_weight=w, h=x, out=x)
+    with pytest.raises(ValueError):
+        ra.radamw_residual_norm_grad(x, x, ra.residual_options(), w, None, grad_x=x)
+    with pytest.raises(ValueError):
+        ra.radamw_balance_loss(x, ids, ra.balance_options(), w, w, w, w, w, w)
+    with pytest.raises(ValueError):
+        ra.radamw_balance_grad(x, 2, ra.balance_options(), w, w, x)
+
+
+# ------------------------------------------------ the plain forms themselves --
+
+def test_generator_vectors():
+    """The known answers of the generator's authors (ten rounds, 4x32)."""
+    ones = 0xFFFFFFFF
+    for counter, key, want in (
+            ((0, 0, 0, 0), (0, 0), (0x6627E8D5, 0xE169C58D, 0xBC57AC4C, 0x9B00DBD8)),
+            ((ones,) * 4, (ones,) * 2, (0x408F276D, 0x41C83B0E, 0xA20BC7C6, 0x6D5451FD)),
+            ((0x243F6A88, 0x85A308D3, 0x13198A2E, 0x03707344), (0xA4093822, 0x299F31D0),
+             (0xD16CFE09, 0x94FDCCEB, 0x5001E420, 0x24126EA1))):
+        assert tuple(int(v) for v in philox(counter, key)) == want
+
+
+def test_mask_is_a_function_of_place():
+    full = keep_mask(40, 100, 0.3, 2 ** 63 + 7, 2 ** 40 + 3)
+    assert torch.equal(full[11:29], keep_mask(18, 100, 0.3, 2 ** 63 + 7, 2 ** 40 + 3, 11))
+    assert torch.equal(full[:, :37], keep_mask(40, 37, 0.3, 2 ** 63 + 7, 2 ** 40 + 3))
+    assert abs(float((~full).double().mean()) - 0.3) < 5 * (0.21 / 4000) ** 0.5
+    assert keep_mask(2, 9, 0.0, 1, 1).all() and not keep_mask(2, 9, 1.0, 1, 1).any()
+    assert keep_factor(0.5) == 2.0 and keep_factor(0.0) == 1.0 and keep_factor(1.0) == 0.0
+    x = torch.randn(5, 9, generator=gen(1))
+    ref, _ = dropout(x, 0.25, 3, 4)
+    assert torch.equal(ref != 0, keep_mask(5, 9, 0.25, 3, 4))
+
+
+def residual_inputs(n=6, dim=11, gates=2):
+    t = [torch.randn(s, generator=gen(i), dtype=DOUBLE) for i, s in
+         enumerate([(n, dim), (n, dim), (gates, dim), (dim,), (dim,), (n, dim), (n, dim)])]
+    return t
+
+
+@pytest.mark.parametrize("post,pre,gates,p", [(True, True, 2, 0.3), (True, False, 0, 0.0), (False, True, 6, 0.4),
+                                              (False, False, 1, 0.5), (True, True, 1, 0.0)])
+def test_plain_residual_gradient(post, pre, gates, p):
+    """backward() against torch's autograd of the formula and against
+    differences of forward()."""
+    n = 6
+    x, y, g, w1, w2, dh, dout = residual_inputs(n, 11, gates or 1)
+    per = -(-n // gates) if gates else None
+    leaves = {"x": x, "branch": y, "gate": g if gates else None, "post": w1 if post else None, "pre": w2 if pre else None}
+    kw = dict(per=per, eps=1e-3, offset=1.0, scale=0.75, p=p, seed=5, counter=9)
+
+    def value(v):
+        f = Residual(v["x"], v["branch"], v["gate"], post=v["post"], pre=v["pre"], **kw).forward()
+        return (f["h"][0] * dh).sum() + ((f["out"][0] * dout).sum() if pre else 0.0), f
+
+    live = {k: None if v is None else v.clone().requires_grad_() for k, v in leaves.items()}
+    total, f = value(live)
+    names = [k for k, v in live.items() if v is not None]
+    auto = dict(zip(names, torch.autograd.grad(total, [live[k] for k in names])))
+    rstd = torch.cat([f["rstd_branch"][0] if post else torch.zeros(n), f["rstd_h"][0] if pre else torch.zeros(n)]).detach()
+    r = Residual(f["h"][0].detach(), y, leaves["gate"], post=leaves["post"], pre=leaves["pre"], **kw)
+    got = r.backward(dh, dout if pre else None, rstd)
+    assert set(got) == set(names)
+    for k in names:
+        assert torch.allclose(got[k][0], auto[k], rtol=1e-10, atol=1e-12), k
+        assert bool((got[k][1] >= 0).all()), k
+        at = (0,) * leaves[k].dim()
+        moved = []
+        for step in (1e-6, -1e-6):
+            v = dict(leaves)
+            v[k] = leaves[k].clone()
+            v[k][at] += step
+            moved.append(value(v)[0])
+        assert math.isclose(float((moved[0] - moved[1]) / 2e-6), float(got[k][0][at]), rel_tol=1e-5, abs_tol=1e-7), k
+
+
+@pytest.mark.parametrize("score,z", [("softmax", 0.0), ("softmax", 0.3), ("sigmoid", 0.0)])
+def test_plain_balance(score, z):
+    n, e, k = 17, 5, 2
+    x = torch.randn((n, e), generator=gen(1), dtype=DOUBLE)
+    ids = torch.randint(0, e, (n, k), generator=gen(2))
+    mask = torch.rand(n, generator=gen(3)) < 0.8
+    bounds, w = [1, 7, 7, 15], torch.tensor([0.5, 2.0, -1.0])
+    z_ = x.clone().requires_grad_()
+    p = z_.softmax(1) if score == "softmax" else z_.sigmoid() / z_.sigmoid().sum(1, keepdim=True)
+    total = 0.0
+    for g in range(3):
+        rows = [t for t in range(bounds[g], bounds[g + 1]) if mask[t]]
+        if not rows:
+            continue
+        c = torch.stack([(ids[rows] == j).sum() for j in range(e)]).double()
+        total = total + w[g].double() * (0.1 * e / (k * len(rows)) * (c * p[rows].mean(0)).sum()
+                                         + z * z_[rows].logsumexp(1).square().mean())
+    got = balance(x, ids, mask, bounds, w, 0.1, z, score, 3.0)
+    assert math.isclose(float(got["total"][0]), float(total.detach()), rel_tol=1e-12)
+    auto, = torch.autograd.grad(total, z_)
+    assert torch.allclose(got["grad"][0], 3 * auto, rtol=1e-10, atol=1e-14)
+    assert bool((got["grad"][1] >= 0).all()) and got["tokens"].tolist() == [int(mask[1:7].sum()), 0, int(mask[7:15].sum())]
