@@ -1,10 +1,17 @@
-"""Autograd forms of the vocabulary operators, for a torch training loop whose
-step is FusedAdamW: the embedding lookup at one end of a model and the policy
-or preference loss at the other.
+"""Autograd forms of the vocabulary and block operators, for a torch training
+loop whose step is FusedAdamW: the embedding lookup at one end of a model, the
+residual stream's dropout and norms around each block, a router's balance
+loss, and the policy or preference loss at the other end.
 
     x = embedding(ids, table, scale=d ** 0.5, grad_buffer=table.grad)
-    total, loss, logp = policy_loss(model(x), labels, advantages, old_logp=old)
-    (total * loss_scale).backward()
+    x = dropout(x, 0.1, seed=run, offset=site(step, 0))
+    y = residual_norm(x, None, pre_weight=norms[0])
+    for i, block in enumerate(blocks):
+        x, y = residual_norm(x, block(y), post_weight=posts[i], pre_weight=norms[i + 1], gate=gates[i], p=0.1,
+                             seed=run, offset=site(step, i + 1))
+    balance, *_ = balance_loss(router_logits, chosen_experts)
+    total, loss, logp = policy_loss(head(y), labels, advantages, old_logp=old)
+    ((total + balance) * loss_scale).backward()
     optimizer.step(gradient_scale=loss_scale)
 
 All arithmetic runs in the library's kernels; these functions shape the
@@ -24,7 +31,7 @@ from torch.autograd.function import once_differentiable
 
 from . import _abi
 
-__all__ = ["embedding", "policy_loss", "preference_loss"]
+__all__ = ["balance_loss", "dropout", "embedding", "policy_loss", "preference_loss", "residual_norm"]
 
 
 def _rows(t: torch.Tensor) -> torch.Tensor:
@@ -253,3 +260,210 @@ def preference_loss(logits: torch.Tensor, labels: torch.Tensor, offsets: torch.T
     return _PreferenceLoss.apply(_rows(logits), flat, offsets.to(flat.dtype).contiguous(),
                                  _flat32(ref_logp, "ref_logp", 2 * pairs), w,
                                  _abi.preference_options(beta, label_smoothing))
+
+
+# ------------------------------------------------------------------ blocks --
+
+class _Dropout(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, opts):
+        ctx.opts = opts
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        _abi.radamw_dropout(x.detach(), out, opts)
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_out):
+        grad = torch.empty(grad_out.shape, dtype=grad_out.dtype, device=grad_out.device)
+        _abi.radamw_dropout(_rows(grad_out), grad, ctx.opts)
+        return grad, None
+
+
+def dropout(x: torch.Tensor, p: float, *, seed: int, offset: int = 0, first_row: int = 0,
+            training: bool = True) -> torch.Tensor:
+    """radamw_dropout of x [..., dim], whose leading dimensions are its rows:
+    x / keep where the generator keeps an element, else 0.
+
+    Which elements are kept depends on ``seed``, ``offset``, the row (counted
+    from ``first_row``) and the column alone, so that a recomputed pass has the
+    same ones; every use of a step and every step needs an offset of its own.
+    No mask is stored.  Without ``training`` x itself is returned."""
+    if not 0.0 <= p <= 1.0:
+        raise ValueError(f"p must be within 0 .. 1 (got {p})")
+    if not training or p == 0.0:
+        return x
+    if x.dim() == 0:
+        raise ValueError("x must have at least one dimension")
+    return _Dropout.apply(_rows(x), _abi.dropout_options(p, seed, offset, first_row)).view(x.shape)
+
+
+class _ResidualNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, branch, gate, post_weight, pre_weight, opts, per, out_dtype):
+        n, dim = x.shape
+        dev = x.device
+        rstd = _empty32((2, n), dev)
+        h = None if branch is None else torch.empty((n, dim), dtype=x.dtype, device=dev)
+        out = None if pre_weight is None else torch.empty((n, dim), dtype=out_dtype, device=dev)
+        given = [None if t is None else t.detach() for t in (x, branch, gate, post_weight, pre_weight)]
+        _abi.radamw_residual_norm(given[0], given[1], opts, gate=given[2], rows_per_gate=per, post_weight=given[3],
+                                  pre_weight=given[4], h=h, out=out, rstd=rstd)
+        # h is read again by the norm before the next block alone
+        ctx.save_for_backward(None if pre_weight is None else x if h is None else h, branch, gate, post_weight,
+                              pre_weight, rstd)
+        ctx.opts, ctx.per = opts, per
+        ctx.set_materialize_grads(False)
+        return h, out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_h, grad_out):
+        h, branch, gate, post_weight, pre_weight, rstd = ctx.saved_tensors
+        like = grad_h if grad_h is not None else grad_out
+        if like is None:
+            return (None,) * 8
+        n, dim = like.shape
+        dev = like.device
+        asked = ctx.needs_input_grad
+
+        def empty(t, wanted=True):
+            return torch.empty(t.shape, dtype=t.dtype, device=dev) if t is not None and wanted else None
+
+        if grad_out is None:  # nothing came through the norm before the next block
+            pre_weight = None
+        stream = h.dtype if h is not None else grad_h.dtype
+        grad_x = torch.empty((n, dim), dtype=stream, device=dev)
+        grad_branch = empty(branch)
+        grad_gate, grad_post, grad_pre = empty(gate, asked[2]), empty(post_weight, asked[3]), empty(pre_weight, asked[4])
+        need = _abi.radamw_residual_grad_workspace_bytes(n, dim, ctx.per or 1)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        _abi.radamw_residual_norm_grad(
+            h, branch, ctx.opts, rstd, workspace, gate=gate, rows_per_gate=ctx.per, post_weight=post_weight,
+            pre_weight=pre_weight, grad_h=None if grad_h is None else _rows(grad_h),
+            grad_out=None if grad_out is None else _rows(grad_out), grad_x=grad_x, grad_branch=grad_branch,
+            grad_gate=grad_gate, grad_post_weight=grad_post, grad_pre_weight=grad_pre)
+        return grad_x, grad_branch, grad_gate, grad_post, grad_pre, None, None, None
+
+
+def _gate_rows(gate: torch.Tensor, shape: torch.Size):
+    """(gate as [rows, dim], rows of the stream that share one)."""
+    g = (1,) * (len(shape) - gate.dim()) + tuple(gate.shape)
+    k = len(shape) - 1
+    while k > 0 and g[k - 1] == 1:
+        k -= 1
+    if len(g) != len(shape) or g[:k] != tuple(shape[:k]) or g[-1] != shape[-1]:
+        raise ValueError(f"gate of shape {tuple(gate.shape)} is not the leading part of {tuple(shape)}: expected its "
+                         "shape with trailing dimensions before the last one (or all) of size 1")
+    per = 1
+    for s in shape[k:-1]:
+        per *= s
+    return _rows(gate), max(1, per)
+
+
+def residual_norm(x: torch.Tensor, branch: Optional[torch.Tensor], *, pre_weight: Optional[torch.Tensor] = None,
+                  post_weight: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                  residual_scale: float = 1.0, eps: float = 1e-6, weight_offset: float = 0.0, p: float = 0.0,
+                  seed: int = 0, offset: int = 0, first_row: int = 0, training: bool = True,
+                  out_dtype: Optional[torch.dtype] = None):
+    """radamw_residual_norm of x and branch [..., dim]: with
+
+        h = x + residual_scale * gate * dropout(norm(branch) * post_weight)
+        out = norm(h) * pre_weight
+
+    (h, out); h alone without a ``pre_weight``; out = norm(x) * pre_weight
+    alone where ``branch`` is None.  No ``post_weight``: the branch as it is.
+    The weights are (weight_offset + weight) [dim], of one dtype.
+
+    ``gate`` broadcasts to x's shape along dimensions before the last: [dim],
+    [batch, 1, dim] for x [batch, length, dim], or x's own shape.  Dropout as
+    in dropout().  x has the branch's dtype or float32; out has the branch's
+    (without a branch ``out_dtype``, by default x's).  Gradients reach x, the
+    branch, the gate and both weights."""
+    if not 0.0 <= p <= 1.0:
+        raise ValueError(f"p must be within 0 .. 1 (got {p})")
+    if branch is None:
+        if pre_weight is None or gate is not None or post_weight is not None:
+            raise ValueError("without a branch there is the norm with pre_weight alone")
+        kind = out_dtype or x.dtype
+    else:
+        if branch.shape != x.shape:
+            raise ValueError(f"branch has shape {tuple(branch.shape)}, expected {tuple(x.shape)}")
+        kind = branch.dtype
+        if out_dtype not in (None, kind):
+            raise ValueError(f"out has the branch's dtype {kind} (got {out_dtype})")
+    if x.dtype not in (kind, torch.float32):
+        raise ValueError(f"x must be {kind} or float32 (got {x.dtype})")
+    for w, what in ((post_weight, "post_weight"), (pre_weight, "pre_weight")):
+        if w is not None and tuple(w.shape) != (x.shape[-1],):
+            raise ValueError(f"{what} has shape {tuple(w.shape)}, expected {(x.shape[-1],)}")
+    rows, per = (None, None) if gate is None else _gate_rows(gate, x.shape)
+    drop = p if training and branch is not None else 0.0
+    opts = _abi.residual_options(eps, weight_offset, residual_scale, drop, seed, offset, first_row)
+    h, out = _ResidualNorm.apply(_rows(x), None if branch is None else _rows(branch), rows,
+                                 None if post_weight is None else post_weight.contiguous(),
+                                 None if pre_weight is None else pre_weight.contiguous(), opts, per, kind)
+    if branch is None:
+        return out.view(x.shape)
+    return h.view(x.shape) if out is None else (h.view(x.shape), out.view(x.shape))
+
+
+class _BalanceLoss(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, ids, mask, offsets, weights, opts):
+        n, experts = logits.shape
+        dev = logits.device
+        groups = weights.numel()
+        total, loss, mean_prob = (_empty32(s, dev) for s in ((), groups, (groups, experts)))
+        counts = torch.empty((groups, experts), dtype=torch.int32, device=dev)
+        tokens = torch.empty(groups, dtype=torch.int32, device=dev)
+        need = _abi.radamw_balance_workspace_bytes(n, experts, groups)
+        _abi.radamw_balance_loss(logits.detach(), ids, opts, total, loss, counts, tokens, mean_prob,
+                                 torch.empty(need, dtype=torch.uint8, device=dev), mask=mask, offsets=offsets,
+                                 weights=weights)
+        ctx.save_for_backward(logits, mask, offsets, weights, counts, tokens)
+        ctx.opts, ctx.top_k = opts, ids.shape[1]
+        ctx.mark_non_differentiable(loss, counts, mean_prob)
+        ctx.set_materialize_grads(False)
+        return total, loss, counts, mean_prob
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_total, *_):
+        if grad_total is None:
+            return (None,) * 6
+        logits, mask, offsets, weights, counts, tokens = ctx.saved_tensors
+        grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        _abi.radamw_balance_grad(logits.detach(), ctx.top_k, ctx.opts, counts, tokens, grad, mask=mask, offsets=offsets,
+                                 weights=weights, upstream=grad_total.to(torch.float32).contiguous())
+        return (grad,) + (None,) * 5
+
+
+def balance_loss(logits: torch.Tensor, ids: torch.Tensor, *, mask: Optional[torch.Tensor] = None,
+                 offsets: Optional[torch.Tensor] = None, weights: Optional[torch.Tensor] = None,
+                 balance_coef: float = 0.01, z_coef: float = 0.0, score: str = "softmax"):
+    """(total, loss, counts, mean_prob) of a router's balance loss and z-loss
+    (radamw_balance_loss) over logits [..., experts] and the chosen experts
+    ids [..., top_k].
+
+    ``mask`` [...] (bool) leaves out padding.  ``offsets`` (groups + 1, device
+    integers) give groups of rows that are balanced each by itself; without
+    them all rows are one group.  ``total`` is differentiable with respect to
+    the logits alone; ``loss`` (groups), ``counts`` [groups, experts] (int32)
+    and ``mean_prob`` [groups, experts] are not.  ``weights`` default to 1 /
+    groups."""
+    if ids.shape[:-1] != logits.shape[:-1]:
+        raise ValueError(f"ids have shape {tuple(ids.shape)}, expected {tuple(logits.shape[:-1])} + (top_k,)")
+    if mask is not None and mask.shape != logits.shape[:-1]:
+        raise ValueError(f"mask has shape {tuple(mask.shape)}, expected {tuple(logits.shape[:-1])}")
+    if offsets is not None and (offsets.dim() != 1 or offsets.numel() < 2):
+        raise ValueError(f"offsets must hold groups + 1 entries (got {tuple(offsets.shape)})")
+    groups = 1 if offsets is None else offsets.numel() - 1
+    if weights is None:
+        w = torch.full((groups,), 1.0 / groups, dtype=torch.float32, device=logits.device)
+    else:
+        w = _flat32(weights, "weights", groups)
+    opts = _abi.balance_options(balance_coef, z_coef, score)
+    chosen = ids.reshape(-1, ids.shape[-1]).contiguous()
+    return _BalanceLoss.apply(_rows(logits), chosen, None if mask is None else mask.reshape(-1).contiguous(),
+                              None if offsets is None else offsets.to(chosen.dtype).contiguous(), w, opts)

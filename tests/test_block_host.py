@@ -264,3 +264,39 @@ def test_plain_balance(score, z):
     auto, = torch.autograd.grad(total, z_)
     assert torch.allclose(got["grad"][0], 3 * auto, rtol=1e-10, atol=1e-14)
     assert bool((got["grad"][1] >= 0).all()) and got["tokens"].tolist() == [int(mask[1:7].sum()), 0, int(mask[7:15].sum())]
+
+
+# ----------------------------------------------------- autograd forms' checks --
+
+def test_functional_argument_checks():
+    from optimizer_step_dl_amd import functional as F
+    x, w = torch.zeros(2, 3, 8), torch.ones(8)
+    for kw in (dict(p=-0.1), dict(p=1.1), dict(p=0.5, seed=-1)):
+        with pytest.raises(ValueError):
+            F.dropout(x, **{**dict(p=0.5, seed=1), **kw})
+    assert F.dropout(x, 0.0, seed=1) is x and F.dropout(x, 0.7, seed=1, training=False) is x
+    with pytest.raises(ValueError):
+        F.dropout(torch.zeros(()), 0.5, seed=1)
+    for kw in (dict(branch=x[:, :2]), dict(branch=None, pre_weight=None), dict(branch=None, gate=w),
+               dict(branch=None, post_weight=w), dict(pre_weight=w[:7]), dict(post_weight=w[None]), dict(p=2.0),
+               dict(branch=x.half()[..., :], x=x.bfloat16()), dict(branch=x.double()), dict(out_dtype=torch.float16),
+               dict(gate=torch.zeros(2, 8)), dict(gate=torch.zeros(3, 8)), dict(gate=torch.zeros(1, 3, 8)),
+               dict(gate=torch.zeros(2, 3, 1)), dict(gate=torch.zeros(1, 2, 3, 8)), dict(eps="a")):
+        with pytest.raises(ValueError):
+            F.residual_norm(**{**dict(x=x, branch=x, pre_weight=w), **kw})
+    ids = torch.zeros(2, 3, 2, dtype=torch.int64)
+    for kw in (dict(ids=ids[:1]), dict(mask=torch.ones(2, dtype=torch.bool)), dict(offsets=torch.zeros(1)),
+               dict(offsets=torch.zeros(2, 2)), dict(weights=torch.ones(2)), dict(score="relu")):
+        with pytest.raises(ValueError):
+            F.balance_loss(**{**dict(logits=x, ids=ids), **kw})
+
+
+def test_gate_shapes():
+    """Gate rows, and the rows of the stream that share one."""
+    from optimizer_step_dl_amd.functional import _gate_rows
+    shape = torch.Size((4, 5, 8))
+    for g, rows, per in (((8,), 1, 20), ((1, 8), 1, 20), ((1, 1, 8), 1, 20), ((4, 1, 8), 4, 5), ((4, 5, 8), 20, 1)):
+        got, p = _gate_rows(torch.zeros(g), shape)
+        assert got.shape == (rows, 8) and p == per
+    assert _gate_rows(torch.zeros(1, 1, 8), torch.Size((1, 6, 8)))[1] == 6
+    assert _gate_rows(torch.zeros(1, 6, 8), torch.Size((1, 6, 8)))[1] == 1
