@@ -15,6 +15,7 @@ namespace radamw {
 // NT lanes hold a row, K pieces of eight each.
 template <int SDT, int BDT, int NT, int K, bool TAIL>
 __global__ __launch_bounds__(row_block<NT>) void residual_norm(ResidualArgs a, int64_t row0) {
+    constexpr bool SPLIT = split_stream<SDT>;
     __shared__ float part[2][row_block<NT> / 64];
     const int lane = threadIdx.x % NT;
     const int32_t dim = static_cast<int32_t>(a.dim);
@@ -22,14 +23,14 @@ __global__ __launch_bounds__(row_block<NT>) void residual_norm(ResidualArgs a, i
     if (t >= a.n) return;  // whole waves; with NT > 64 whole workgroups
     const char *xr = elem_at(a.x, SDT, t * a.x_stride), *yr = elem_at(a.branch, BDT, t * a.branch_stride);
     const char *gr = elem_at(a.gate, a.gate_dt, a.gate ? t / a.per * a.gate_stride : 0);
-    const auto post_at = [&](int32_t e) {
-        return a.post ? load_any<TAIL>(static_cast<const char *>(a.post), a.weight_dt, e, dim, a.weight_offset) : all_of(1.0f);
+    const auto post_at = [&](Piece e) {
+        return a.post ? load_weight<SPLIT, TAIL>(a.post, a.weight_dt, e, dim, a.weight_offset) : all_of(1.0f);
     };
-    const auto pre_at = [&](int32_t e) {
-        return load_any<TAIL>(static_cast<const char *>(a.pre), a.weight_dt, e, dim, a.weight_offset);
+    const auto pre_at = [&](Piece e) {
+        return load_weight<SPLIT, TAIL>(a.pre, a.weight_dt, e, dim, a.weight_offset);
     };
-    const auto gate_at = [&](int32_t e) {
-        return a.gate ? load_any<TAIL>(gr, a.gate_dt, e, dim, 0.0f) : all_of(1.0f);
+    const auto gate_at = [&](Piece e) {
+        return a.gate ? load_weight<SPLIT, TAIL>(gr, a.gate_dt, e, dim, 0.0f) : all_of(1.0f);
     };
     Raw8<SDT> x[K];
     Raw8<BDT> y[K];
@@ -37,11 +38,11 @@ __global__ __launch_bounds__(row_block<NT>) void residual_norm(ResidualArgs a, i
     f32x8 gate, post, pre;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int32_t e = (lane + k * NT) * 8;
+        const Piece e = piece_at<SPLIT, NT>(lane, k);
         y[k] = Raw8<BDT>{};
-        if (e >= dim) continue;
-        if (a.branch) y[k] = load_piece<BDT, TAIL>(yr, e, dim);
-        x[k] = load_piece<SDT, TAIL>(xr, e, dim);
+        if (e.e >= dim) continue;
+        if (a.branch) y[k] = load_piece<BDT, SPLIT, TAIL>(yr, e, dim);
+        x[k] = load_piece<SDT, SPLIT, TAIL>(xr, e, dim);
         if constexpr (K == 1) {
             post = post_at(e);
             gate = gate_at(e);
@@ -67,8 +68,8 @@ __global__ __launch_bounds__(row_block<NT>) void residual_norm(ResidualArgs a, i
     float s = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int32_t e = (lane + k * NT) * 8;
-        if (e >= dim) continue;
+        const Piece e = piece_at<SPLIT, NT>(lane, k);
+        if (e.e >= dim) continue;
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[k][j] = raw_value<SDT>(x[k], j);
         if (a.branch) {
@@ -77,13 +78,13 @@ __global__ __launch_bounds__(row_block<NT>) void residual_norm(ResidualArgs a, i
                 gate = gate_at(e);
             }
             u32x4 words = {0, 0, 0, 0};
-            if (a.drop.threshold) words = random_words(static_cast<uint32_t>(e >> 3), static_cast<uint32_t>(t), a.drop);
+            if (a.drop.threshold) words = piece_words<SPLIT>(e, t, a.drop);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float u = raw_value<BDT>(y[k], j) * rb * post[j] * gate[j] * a.drop.factor;
                 h[k][j] = __builtin_fmaf(a.scale, kept(words, j, a.drop.threshold) ? u : 0.0f, h[k][j]);
             }
-            store_piece<SDT, TAIL>(elem_at(a.h, SDT, t * a.h_stride), e, dim, h[k]);
+            store_piece<SDT, SPLIT, TAIL>(elem_at(a.h, SDT, t * a.h_stride), e, dim, h[k]);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) s = __builtin_fmaf(h[k][j], h[k][j], s);
@@ -94,25 +95,123 @@ __global__ __launch_bounds__(row_block<NT>) void residual_norm(ResidualArgs a, i
     if (a.rstd && lane == 0) a.rstd[a.n + t] = rh;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int32_t e = (lane + k * NT) * 8;
-        if (e >= dim) continue;
+        const Piece e = piece_at<SPLIT, NT>(lane, k);
+        if (e.e >= dim) continue;
         if constexpr (K > 1) pre = pre_at(e);
         f32x8 v;
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = h[k][j] * rh * pre[j];
-        store_piece<BDT, TAIL>(elem_at(a.out, BDT, t * a.out_stride), e, dim, v);
+        store_piece<BDT, SPLIT, TAIL>(elem_at(a.out, BDT, t * a.out_stride), e, dim, v);
     }
 }
 
+// Two rows at a time, a piece of each to a lane: they share the weights' loads
+// and the barriers.
+template <int SDT, int BDT, int NT, bool TAIL>
+__global__ __launch_bounds__(row_block<NT>) void residual_norm_pair(ResidualArgs a, int64_t row0) {
+    constexpr bool SPLIT = split_stream<SDT>;
+    __shared__ float part[2][2 * row_block<NT> / 64];
+    const int lane = threadIdx.x % NT;
+    const int32_t dim = static_cast<int32_t>(a.dim);
+    const Piece e = piece_at<SPLIT, NT>(lane, 0);
+    const int64_t t0 = row0 + (int64_t(blockIdx.x) * (row_block<NT> / NT) + wave_row<NT>()) * 2;
+    if (t0 >= a.n) return;  // whole waves; with NT > 64 whole workgroups
+    // behind the last row that row is read again and nothing stored
+    const bool both = t0 + 1 < a.n, here = e.e < dim;
+    const int64_t t[2] = {t0, both ? t0 + 1 : t0};
+    Raw8<SDT> x[2];
+    Raw8<BDT> y[2] = {};
+    f32x8 gate[2], post, pre;
+    post = gate[0] = gate[1] = all_of(1.0f);
+    if (here) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            if (a.branch) y[m] = load_piece<BDT, SPLIT, TAIL>(elem_at(a.branch, BDT, t[m] * a.branch_stride), e, dim);
+            x[m] = load_piece<SDT, SPLIT, TAIL>(elem_at(a.x, SDT, t[m] * a.x_stride), e, dim);
+        }
+        if (a.post) post = load_weight<SPLIT, TAIL>(a.post, a.weight_dt, e, dim, a.weight_offset);
+        if (a.gate) {
+            const uint32_t g0 = static_cast<uint32_t>(t[0]) / static_cast<uint32_t>(a.per),
+                           g1 = static_cast<uint32_t>(t[1]) / static_cast<uint32_t>(a.per);
+            gate[0] = load_weight<SPLIT, TAIL>(elem_at(a.gate, a.gate_dt, g0 * a.gate_stride), a.gate_dt, e, dim, 0.0f);
+            gate[1] = g1 == g0 ? gate[0]
+                               : load_weight<SPLIT, TAIL>(elem_at(a.gate, a.gate_dt, g1 * a.gate_stride), a.gate_dt, e, dim, 0.0f);
+        }
+        if (a.pre) pre = load_weight<SPLIT, TAIL>(a.pre, a.weight_dt, e, dim, a.weight_offset);
+    }
+    const float inv_dim = 1.0f / static_cast<float>(dim);
+    float rb[2] = {1.0f, 1.0f}, s[2] = {0.0f, 0.0f};
+    if (a.post) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float v = raw_value<BDT>(y[m], j);
+                s[m] = __builtin_fmaf(v, v, s[m]);
+            }
+        row_sums<NT>(s[0], s[1], part[0]);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            rb[m] = rsqrtf(__builtin_fmaf(s[m], inv_dim, a.eps));
+            if (a.rstd && lane == 0) a.rstd[t[m]] = rb[m];
+            s[m] = 0.0f;
+        }
+    }
+    f32x8 h[2];
+    if (here) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) h[m][j] = raw_value<SDT>(x[m], j);
+            if (a.branch) {
+                u32x4 words = {0, 0, 0, 0};
+                if (a.drop.threshold)
+                    words = piece_words<SPLIT>(e, t[m], a.drop);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float u = raw_value<BDT>(y[m], j) * rb[m] * post[j] * gate[m][j] * a.drop.factor;
+                    h[m][j] = __builtin_fmaf(a.scale, kept(words, j, a.drop.threshold) ? u : 0.0f, h[m][j]);
+                }
+                if (m == 0 || both) store_piece<SDT, SPLIT, TAIL>(elem_at(a.h, SDT, t[m] * a.h_stride), e, dim, h[m]);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[m] = __builtin_fmaf(h[m][j], h[m][j], s[m]);
+        }
+    }
+    if (!a.pre) return;
+    row_sums<NT>(s[0], s[1], part[1]);
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        const float rh = rsqrtf(__builtin_fmaf(s[m], inv_dim, a.eps));
+        if (a.rstd && lane == 0) a.rstd[a.n + t[m]] = rh;
+        if (!here || (m == 1 && !both)) continue;
+        f32x8 v;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = h[m][j] * rh * pre[j];
+        store_piece<BDT, SPLIT, TAIL>(elem_at(a.out, BDT, t[m] * a.out_stride), e, dim, v);
+    }
+}
+
+// Two rows at a time where that leaves four workgroups per CU: 8192 x 4096
+// (FP32 stream, BF16 branch, FP32 weights) takes 75 us, against 80 us, 65536 x
+// 2048 BF16 180 against 195 us.  Wider rows have no registers for two.
+constexpr int64_t PAIR_ROWS = 2048;
 // Rows of one launch.
 constexpr int64_t RESIDUAL_LAUNCH_ROWS = int64_t(1) << 21;
 
 template <int SDT, int BDT, int NT, int K>
 static hipError_t residual_at(const ResidualArgs &a, hipStream_t stream, int *launched) {
-    const auto kernel = a.dim % 8 ? residual_norm<SDT, BDT, NT, K, true> : residual_norm<SDT, BDT, NT, K, false>;
+    auto kernel = a.dim % 8 ? residual_norm<SDT, BDT, NT, K, true> : residual_norm<SDT, BDT, NT, K, false>;
+    int rows_of_block = row_block<NT> / NT;
+    if constexpr (K == 1) {
+        if (a.n >= PAIR_ROWS) {
+            kernel = a.dim % 8 ? residual_norm_pair<SDT, BDT, NT, true> : residual_norm_pair<SDT, BDT, NT, false>;
+            rows_of_block *= 2;
+        }
+    }
     for (int64_t row0 = 0; row0 < a.n; row0 += RESIDUAL_LAUNCH_ROWS) {
         const int64_t rows = a.n - row0 < RESIDUAL_LAUNCH_ROWS ? a.n - row0 : RESIDUAL_LAUNCH_ROWS;
-        hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(ceil_div(rows, row_block<NT> / NT))), dim3(row_block<NT>), 0,
+        hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(ceil_div(rows, rows_of_block))), dim3(row_block<NT>), 0,
                            stream, a, row0);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
@@ -124,7 +223,9 @@ static hipError_t residual_at(const ResidualArgs &a, hipStream_t stream, int *la
 template <int SDT, int BDT>
 static hipError_t residual_shape(const ResidualArgs &a, hipStream_t stream, int *launched) {
 #define RADAMW_CALL(NT, K) return residual_at<SDT, BDT, NT, K>(a, stream, launched)
-    RADAMW_ROW_SHAPES(a.dim, RADAMW_CALL)
+    // 32768 x 8192 BF16 rows take 363 us, against 432 us with 1024 lanes of one
+    // piece and 381 us with 256 of four
+    RADAMW_ROW_SHAPES(a.dim, RADAMW_CALL, RADAMW_CALL(512, 2))
 #undef RADAMW_CALL
 }
 

@@ -18,15 +18,19 @@
 
 namespace radamw {
 
-// The most workers (each a row's lanes), and the least rows of one where
-// there are more rows than CUs: a worker leaves 4 bytes per column and sum,
-// read again by the join, against 12 to 24 bytes per column and row.
-constexpr int64_t GRAD_WORKERS = 1024;
+// Waves per CU of the gradient (128 registers each leave room for sixteen), and
+// the least rows of a worker (a row's lanes) where there are more rows than
+// CUs: a worker leaves 4 bytes per column and sum, read again by the join,
+// against 12 to 24 bytes per column and row.
+constexpr int64_t GRAD_WAVES = 16;
 constexpr int64_t GRAD_ROWS = 4;
 
 ResidualPlan residual_plan(int64_t n, int64_t dim, int64_t) {
     ResidualPlan p{};
-    const int64_t most = n < 256 ? n : n / GRAD_ROWS < 256 ? 256 : n / GRAD_ROWS < GRAD_WORKERS ? n / GRAD_ROWS : GRAD_WORKERS;
+    int64_t lanes = 64;
+    while (lanes < 1024 && lanes * 8 < dim) lanes *= 2;
+    const int64_t resident = 256 * GRAD_WAVES * 64 / lanes;
+    const int64_t most = n < 256 ? n : n / GRAD_ROWS < 256 ? 256 : n / GRAD_ROWS < resident ? n / GRAD_ROWS : resident;
     p.rows = n > 0 ? ceil_div(n, most) : 1;
     p.workers = ceil_div(n, p.rows);
     p.width = ceil_div(dim, 64) * 64;
@@ -39,172 +43,313 @@ ResidualPlan residual_plan(int64_t n, int64_t dim, int64_t) {
 }
 
 // A worker's column sums, whole pieces: a partial row has room for them.
-template <int NT, int K>
+template <bool SPLIT, int NT, int K>
 __device__ __forceinline__ void put_partial(char *base, int64_t slot, int64_t width, int lane, const f32x8 (&acc)[K]) {
     float *row = reinterpret_cast<float *>(base) + slot * width;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int32_t e = (lane + k * NT) * 8;
-        if (e < width) store8<G_F32>(row, e, acc[k]);
+        const Piece e = piece_at<SPLIT, NT>(lane, k);
+        const f32x4 lo = {acc[k][0], acc[k][1], acc[k][2], acc[k][3]}, hi = {acc[k][4], acc[k][5], acc[k][6], acc[k][7]};
+        if (e.e < width) store_chunk<G_F32>(row, e.e, __builtin_bit_cast(u32x4, lo));
+        if (e.e2 < width) store_chunk<G_F32>(row, e.e2, __builtin_bit_cast(u32x4, hi));
     }
 }
 
-// One worker's rows, in order.  The gate's sum is one per gate row: where the
-// gate row's rows all belong to this worker it is stored, else it is left in
-// slot 0 (the gate row began before this worker) or 1 (it goes on behind it).
-template <int SDT, int BDT, int NT, int K, bool TAIL>
-__global__ __launch_bounds__(row_block<NT>) void residual_norm_grad(ResidualGradArgs a, ResidualPlan p) {
-    __shared__ float part[2][row_block<NT> / 64];
-    const int lane = threadIdx.x % NT;
-    const int32_t dim = static_cast<int32_t>(a.dim);
-    const int64_t w = int64_t(blockIdx.x) * (row_block<NT> / NT) + wave_row<NT>();
-    const int64_t begin = w * p.rows, end = begin + p.rows < a.n ? begin + p.rows : a.n;
-    if (begin >= end) return;  // whole waves; with NT > 64 whole workgroups
-    const float inv_dim = 1.0f / static_cast<float>(dim);
-    const float drop_scale = a.scale * a.drop.factor;
-    f32x8 post[K], pre[K], gate[K], sum_post[K], sum_pre[K], sum_gate[K];
+// Parts of a call, as bits.
+// EACH_ROW: every row has a gate row of its own; EACH_GATE and SUM_GATE: the
+// gate's gradient is asked for, by row or summed.
+enum : uint32_t {
+    HAS_PRE = 1, HAS_POST = 2, HAS_GATE = 4, HAS_BRANCH = 8, HAS_GRAD_H = 16, EACH_ROW = 32, EACH_GATE = 64, SUM_GATE = 128
+};
+
+// What a lane reads of one row.
+template <int SDT, int BDT, int K>
+struct GradRow {
     Raw8<BDT> g[K], y[K];
     Raw8<SDT> h[K], dh[K];
+    Any8 gate[K];
+};
+
+// The kernel's arguments where the hardware has put them, at its first
+// argument's place.  Read through a pointer that the compiler takes for a new
+// one at every row, they need scalar registers only where they are used; kept
+// over the whole loop they were 60 to 120 registers too many, each spilled to
+// a vector lane and back.
+typedef const __attribute__((address_space(4))) ResidualGradArgs *GradArgsPtr;
+__device__ __forceinline__ GradArgsPtr args_again(GradArgsPtr p) {
+    asm volatile("" : "+s"(p));
+    return p;
+}
+
+// A value that the kernel does not write, by a scalar load: a vector load would
+// be waited for with the next row's, which are issued before it.
+__device__ __forceinline__ float row_constant(const float *p, int64_t i) {
+    return ((const __attribute__((address_space(4))) float *)p)[i];
+}
+
+// One worker's rows, in order.  AHEAD: the next row's loads are under way
+// while this row's sums are formed.  The weights wait in LDS, each lane's own,
+// so that the registers hold the column sums and the rows; of lanes with two
+// pieces the weights' sums are in LDS instead.  The gate's sum is one per gate
+// row: where the gate row's rows all belong to this worker it is stored, else
+// it is left in slot 0 (the gate row began before this worker) or 1 (it goes
+// on behind it).
+//
+// KNOWN: the parts that are known to be there, all lanes with columns.  Only
+// then is the number of stores behind the next row's loads known as well, so
+// that those loads are waited for without the stores, with which they share a
+// counter; else 0.
+template <int SDT, int BDT, int NT, int K, bool TAIL, uint32_t KNOWN>
+__global__ __launch_bounds__(row_block<NT>, 4) void residual_norm_grad(ResidualGradArgs args, ResidualPlan p,
+                                                                       uint32_t parts) {
+    constexpr bool SPLIT = split_stream<SDT>;
+    // an FP32 row and the next one have the registers only where parts are
+    // known to be absent; with a gate row for each row it costs more than it
+    // gives (32768 x 8192 BF16: 850 us, against 802 us)
+    constexpr bool AHEAD = K == 1 && (KNOWN ? !(KNOWN & EACH_ROW) : SDT != G_F32);
+    constexpr uint32_t RARE = HAS_GATE | SUM_GATE;  // of no load or store in most rows
+    const uint32_t has = KNOWN ? KNOWN | (parts & RARE) : parts;
+    constexpr int BLOCK = row_block<NT>, WAVES = BLOCK / 64;
+    __shared__ float part[2][2][WAVES];
+    // K == 1: weights; K == 2: sums of both; K == 4: sums of the norm behind the stream's sum
+    __shared__ f32x4 own[K == 1 ? 4 : 8][BLOCK];
+    const GradArgsPtr kernarg = (GradArgsPtr)__builtin_amdgcn_kernarg_segment_ptr();
+    const int lane = threadIdx.x % NT;
+    const int32_t dim = KNOWN ? NT * K * 8 : static_cast<int32_t>(args.dim);
+    const int64_t w = int64_t(blockIdx.x) * (BLOCK / NT) + wave_row<NT>();
+    const int64_t begin = w * p.rows, end = begin + p.rows < args.n ? begin + p.rows : args.n;
+    if (begin >= end) return;  // whole waves; with NT > 64 whole workgroups
+    const float inv_dim = 1.0f / static_cast<float>(dim);
+    f32x8 sum_post[K], sum_pre[K], sum_gate[K];
+    GradRow<SDT, BDT, K> row, next;
+    const auto put_own = [&](int i, f32x8 v) {
+        own[2 * i][threadIdx.x] = f32x4{v[0], v[1], v[2], v[3]};
+        own[2 * i + 1][threadIdx.x] = f32x4{v[4], v[5], v[6], v[7]};
+    };
+    const auto get_own = [&](int i) {
+        const f32x4 lo = own[2 * i][threadIdx.x], hi = own[2 * i + 1][threadIdx.x];
+        return f32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    };
+    // the weights of piece k: 0 behind the branch, 1 behind the stream's sum
+    const auto global_weight = [&](GradArgsPtr a, int which, Piece e) -> f32x8 {
+        if (!(has & (which ? HAS_PRE : HAS_POST)) || e.e >= dim) return all_of(1.0f);
+        return load_weight<SPLIT, TAIL>(which ? a->pre : a->post, a->weight_dt, e, dim, a->weight_offset);
+    };
+    const auto weight = [&](GradArgsPtr a, int which, Piece e) -> f32x8 {
+        if constexpr (K == 1) return get_own(which);
+        else return global_weight(a, which, e);
+    };
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int32_t e = (lane + k * NT) * 8;
-        post[k] = pre[k] = gate[k] = all_of(1.0f);
+        const Piece e = piece_at<SPLIT, NT>(lane, k);
         sum_post[k] = sum_pre[k] = sum_gate[k] = f32x8{};
-        g[k] = y[k] = Raw8<BDT>{};
-        h[k] = dh[k] = Raw8<SDT>{};
-        if (e >= dim) continue;
-        if (a.post) post[k] = load_any<TAIL>(static_cast<const char *>(a.post), a.weight_dt, e, dim, a.weight_offset);
-        if (a.pre) pre[k] = load_any<TAIL>(static_cast<const char *>(a.pre), a.weight_dt, e, dim, a.weight_offset);
-    }
-    // the gate row of row t, and the first row behind it
-    int64_t group = a.gate ? begin / a.per : 0, next = begin;
-    for (int64_t t = begin; t < end; ++t) {
-        if (a.gate && t == next) {
-            if (t != begin) ++group;
-            next = (group + 1) * a.per;
-            const char *row = elem_at(a.gate, a.gate_dt, group * a.gate_stride);
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const int32_t e = (lane + k * NT) * 8;
-                if (e < dim) gate[k] = load_any<TAIL>(row, a.gate_dt, e, dim, 0.0f);
-            }
+        row.g[k] = row.y[k] = Raw8<BDT>{};
+        row.h[k] = row.dh[k] = Raw8<SDT>{};
+        row.gate[k] = Any8{};
+        if constexpr (K == 1) {
+            put_own(0, global_weight(kernarg, 0, e));
+            put_own(1, global_weight(kernarg, 1, e));
+        } else if constexpr (K == 2) {
+            put_own(k, f32x8{});
+            put_own(2 + k, f32x8{});
+        } else {
+            put_own(k, f32x8{});
         }
+    }
+    // adds to piece k's sum, where it is held
+    const auto add_pre = [&](int k, f32x8 v) {
+        if constexpr (K == 1) sum_pre[k] += v;
+        else put_own(k, get_own(k) + v);
+    };
+    const auto add_post = [&](int k, f32x8 v) {
+        if constexpr (K == 2) put_own(2 + k, get_own(2 + k) + v);
+        else sum_post[k] += v;
+    };
+    const auto load_gate = [&](GradArgsPtr a, GradRow<SDT, BDT, K> &r, int64_t group) {
+        const char *from = elem_at(a->gate, a->gate_dt, group * a->gate_stride);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int32_t e = (lane + k * NT) * 8;
-            if (e >= dim) continue;
-            if (a.pre) {
-                g[k] = load_piece<BDT, TAIL>(elem_at(a.grad_out, BDT, t * a.grad_out_stride), e, dim);
-                h[k] = load_piece<SDT, TAIL>(elem_at(a.h, SDT, t * a.h_stride), e, dim);
+            const Piece e = piece_at<SPLIT, NT>(lane, k);
+            if (e.e < dim) r.gate[k] = load_any<SPLIT, TAIL>(from, a->gate_dt, e, dim);
+        }
+    };
+    const auto load = [&](GradArgsPtr a, GradRow<SDT, BDT, K> &r, int64_t t) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const Piece e = piece_at<SPLIT, NT>(lane, k);
+            if (e.e >= dim) continue;
+            if (has & HAS_PRE) {
+                r.g[k] = load_piece<BDT, SPLIT, TAIL>(elem_at(a->grad_out, BDT, t * a->grad_out_stride), e, dim);
+                r.h[k] = load_piece<SDT, SPLIT, TAIL>(elem_at(a->h, SDT, t * a->h_stride), e, dim);
             }
-            if (a.grad_h) dh[k] = load_piece<SDT, TAIL>(elem_at(a.grad_h, SDT, t * a.grad_h_stride), e, dim);
-            if (a.branch) y[k] = load_piece<BDT, TAIL>(elem_at(a.branch, BDT, t * a.branch_stride), e, dim);
+            if (has & HAS_GRAD_H)
+                r.dh[k] = load_piece<SDT, SPLIT, TAIL>(elem_at(a->grad_h, SDT, t * a->grad_h_stride), e, dim);
+            if (has & HAS_BRANCH)
+                r.y[k] = load_piece<BDT, SPLIT, TAIL>(elem_at(a->branch, BDT, t * a->branch_stride), e, dim);
+        }
+        if (has & EACH_ROW) load_gate(a, r, t);
+    };
+    if constexpr (AHEAD) {
+        next = row;
+        load(kernarg, next, begin);
+    }
+    // the gate row of row t, and the first row behind it
+    int64_t group = has & HAS_GATE ? begin / args.per : 0, behind = begin;
+    int odd = 0;
+    for (int64_t t = begin; t < end; ++t, odd ^= 1) {
+        const GradArgsPtr a = args_again(kernarg);
+        if constexpr (AHEAD) {
+            row.g[0] = next.g[0];
+            row.y[0] = next.y[0];
+            row.h[0] = next.h[0];
+            row.dh[0] = next.dh[0];
+            if (has & EACH_ROW) row.gate[0] = next.gate[0];
+            if (t + 1 < end) load(a, next, t + 1);
+        } else {
+            load(a, row, t);
+        }
+        if ((has & HAS_GATE) && t == behind) {
+            if (t != begin) ++group;
+            behind = (group + 1) * a->per;
+            if (!(has & EACH_ROW)) load_gate(a, row, group);
         }
         // D, and the sums of the norm behind the stream's sum
         float rh = 0.0f, mean = 0.0f;
-        if (a.pre) {
-            rh = a.rstd[a.n + t];
+        if (has & HAS_PRE) {
+            rh = row_constant(a->rstd, a->n + t);
             float s = 0.0f;
 #pragma unroll
-            for (int k = 0; k < K; ++k)
+            for (int k = 0; k < K; ++k) {
+                const f32x8 pre = weight(a, 1, piece_at<SPLIT, NT>(lane, k));
+                f32x8 c;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float c = raw_value<BDT>(g[k], j) * (raw_value<SDT>(h[k], j) * rh);
-                    sum_pre[k][j] += c;
-                    s = __builtin_fmaf(c, pre[k][j], s);
+                    c[j] = raw_value<BDT>(row.g[k], j) * (raw_value<SDT>(row.h[k], j) * rh);
+                    s = __builtin_fmaf(c[j], pre[j], s);
                 }
-            mean = row_sum<NT>(s, part[0]) * inv_dim;
+                add_pre(k, c);
+            }
+            mean = row_sum<NT>(s, part[odd][0]) * inv_dim;
         }
-        const float rb = a.post ? a.rstd[t] : 1.0f;
+        const float rb = has & HAS_POST ? row_constant(a->rstd, t) : 1.0f;
         float s = 0.0f;
         f32x8 du[K];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int32_t e = (lane + k * NT) * 8;
-            if (e >= dim) continue;
+            const Piece e = piece_at<SPLIT, NT>(lane, k);
+            if (e.e >= dim) continue;
             f32x8 d;
+            const f32x8 pre = weight(a, 1, e);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float q = raw_value<BDT>(g[k], j) * pre[k][j], hat = raw_value<SDT>(h[k], j) * rh;
-                d[j] = __builtin_fmaf(rh, __builtin_fmaf(-hat, mean, q), raw_value<SDT>(dh[k], j));
+                const float q = raw_value<BDT>(row.g[k], j) * pre[j], hat = raw_value<SDT>(row.h[k], j) * rh;
+                d[j] = __builtin_fmaf(rh, __builtin_fmaf(-hat, mean, q), raw_value<SDT>(row.dh[k], j));
             }
-            store_piece<SDT, TAIL>(elem_at(a.grad_x, SDT, t * a.grad_x_stride), e, dim, d);
-            if (!a.branch) continue;
-            u32x4 words = {0, 0, 0, 0};
-            if (a.drop.threshold) words = random_words(static_cast<uint32_t>(e >> 3), static_cast<uint32_t>(t), a.drop);
-            f32x8 dg;
+            store_piece<SDT, SPLIT, TAIL>(elem_at(a->grad_x, SDT, t * a->grad_x_stride), e, dim, d);
+            if (!(has & HAS_BRANCH)) continue;
+            f32x8 gate = has & HAS_GATE ? any_values(row.gate[k], a->gate_dt, 0.0f) : all_of(1.0f), hat;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                // a dropped place passes nothing on, whatever the branch holds there
-                const bool keep = kept(words, j, a.drop.threshold);
-                const float hat = raw_value<BDT>(y[k], j) * rb, b = d[j] * drop_scale;
-                dg[j] = keep ? b * (hat * post[k][j]) : 0.0f;
-                sum_gate[k][j] += dg[j];
-                const float c = keep ? b * gate[k][j] : 0.0f;
-                sum_post[k][j] = __builtin_fmaf(c, hat, sum_post[k][j]);
-                du[k][j] = c * post[k][j];
-                s = __builtin_fmaf(du[k][j], hat, s);
+                hat[j] = raw_value<BDT>(row.y[k], j) * rb;
+                d[j] *= a->scale;
             }
-            if (a.grad_gate && a.per == 1)
-                store_any<TAIL>(elem_at(a.grad_gate, a.gate_dt, t * a.grad_gate_stride), a.gate_dt, e, dim, dg);
+            if (a->drop.threshold) {
+                // a dropped place passes nothing on, whatever the branch and the gate hold there
+                const DropArgs drop = {a->drop.key0, a->drop.key1, a->drop.off0, a->drop.off1, a->drop.first_row,
+                                       a->drop.threshold, a->drop.factor};
+                const u32x4 words = piece_words<SPLIT>(e, t, drop);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const bool keep = kept(words, j, drop.threshold);
+                    d[j] = keep ? d[j] * drop.factor : 0.0f;
+                    hat[j] = keep ? hat[j] : 0.0f;
+                    gate[j] = keep ? gate[j] : 0.0f;
+                }
+            }
+            const f32x8 post = weight(a, 0, e);
+            f32x8 dg, c;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                dg[j] = d[j] * (hat[j] * post[j]);
+                du[k][j] = d[j] * gate[j];
+                c[j] = du[k][j] * hat[j];
+                du[k][j] *= post[j];
+                s = __builtin_fmaf(c[j], post[j], s);
+            }
+            if (has & HAS_POST) add_post(k, c);
+            if (has & EACH_GATE)
+                store_any<SPLIT, TAIL>(elem_at(a->grad_gate, a->gate_dt, t * a->grad_gate_stride), a->gate_dt, e, dim, dg);
+            if (has & SUM_GATE) sum_gate[k] += dg;
         }
-        if (a.branch) {
+        if (has & HAS_BRANCH) {
             float mb = 0.0f;
-            if (a.post) mb = row_sum<NT>(s, part[1]) * inv_dim * rb;
+            if (has & HAS_POST) mb = row_sum<NT>(s, part[odd][1]) * inv_dim * rb;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                const int32_t e = (lane + k * NT) * 8;
-                if (e >= dim) continue;
-                if (a.post) {
+                const Piece e = piece_at<SPLIT, NT>(lane, k);
+                if (e.e >= dim) continue;
+                if (has & HAS_POST) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        du[k][j] = rb * __builtin_fmaf(-raw_value<BDT>(y[k], j), mb, du[k][j]);
+                        du[k][j] = rb * __builtin_fmaf(-raw_value<BDT>(row.y[k], j), mb, du[k][j]);
                 }
-                store_piece<BDT, TAIL>(elem_at(a.grad_branch, BDT, t * a.grad_branch_stride), e, dim, du[k]);
+                store_piece<BDT, SPLIT, TAIL>(elem_at(a->grad_branch, BDT, t * a->grad_branch_stride), e, dim, du[k]);
             }
         }
-        if constexpr (NT > 64) {
-            // the next row's first sum writes part[0] again: with one norm
-            // alone no other barrier stands between its reads and that write
-            if (!(a.pre && a.post)) __syncthreads();
-        }
-        if (a.grad_gate && (t + 1 == end || t + 1 == next)) {
-            const int64_t from = group * a.per, to = next < a.n ? next : a.n;
-            if (a.per == 1) {
-                // stored above
-            } else if (from >= begin && to <= end) {
-                char *row = elem_at(a.grad_gate, a.gate_dt, group * a.grad_gate_stride);
+        if ((has & SUM_GATE) && (t + 1 == end || t + 1 == behind)) {
+            const int64_t from = group * a->per, to = behind < a->n ? behind : a->n;
+            if (from >= begin && to <= end) {
+                char *out = elem_at(a->grad_gate, a->gate_dt, group * a->grad_gate_stride);
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
-                    const int32_t e = (lane + k * NT) * 8;
-                    if (e < dim) store_any<TAIL>(row, a.gate_dt, e, dim, sum_gate[k]);
+                    const Piece e = piece_at<SPLIT, NT>(lane, k);
+                    if (e.e < dim) store_any<SPLIT, TAIL>(out, a->gate_dt, e, dim, sum_gate[k]);
                 }
             } else {
-                put_partial<NT>(a.workspace + p.gate, 2 * w + (from >= begin), p.width, lane, sum_gate);
+                put_partial<SPLIT, NT>(a->workspace + p.gate, 2 * w + (from >= begin), p.width, lane, sum_gate);
             }
 #pragma unroll
             for (int k = 0; k < K; ++k) sum_gate[k] = f32x8{};
         }
     }
-    if (a.grad_post) put_partial<NT>(a.workspace + p.post, w, p.width, lane, sum_post);
-    if (a.grad_pre) put_partial<NT>(a.workspace + p.pre, w, p.width, lane, sum_pre);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        if constexpr (K > 1) sum_pre[k] = get_own(k);
+        if constexpr (K == 2) sum_post[k] = get_own(2 + k);
+    }
+    if (args.grad_post) put_partial<SPLIT, NT>(args.workspace + p.post, w, p.width, lane, sum_post);
+    if (args.grad_pre) put_partial<SPLIT, NT>(args.workspace + p.pre, w, p.width, lane, sum_pre);
 }
 
-// Sums of partial rows, 64 columns to a workgroup: 16 lanes of four columns,
-// 16 strips of partial rows; FP64.
+// Sums of partial rows in FP64, 32 columns (a cache line) to a workgroup: 8
+// lanes of four columns, 32 strips of partial rows.
 constexpr int JOIN_BLOCK = 256;
-constexpr int JOIN_COLUMNS = 64;
+constexpr int JOIN_COLUMNS = 32;
+constexpr int JOIN_STRIPS = JOIN_BLOCK / (JOIN_COLUMNS / 4);
 
 __device__ __forceinline__ void join_rows(const float *first, const float *rest, int64_t count, int64_t step, int64_t dim,
                                           void *out, int32_t dt, int64_t row) {
     // partial row 0 is `first`, partial row i > 0 is rest + (i - 1) * step
-    __shared__ double strip[16][JOIN_COLUMNS];
-    const int c = (threadIdx.x & 15) * 4, s = threadIdx.x >> 4;
+    __shared__ double strip[JOIN_STRIPS][JOIN_COLUMNS];
+    const int c = (threadIdx.x % (JOIN_COLUMNS / 4)) * 4, s = threadIdx.x / (JOIN_COLUMNS / 4);
     const int64_t e = int64_t(blockIdx.x) * JOIN_COLUMNS + c;
-    double acc[4] = {0.0, 0.0, 0.0, 0.0};
-    for (int64_t i = s; i < count; i += 16) {
+    const auto at = [&](int64_t i) {
         const float *src = i == 0 ? first : rest + (i - 1) * step;
-        const f32x4 v = *(const RADAMW_GLOBAL f32x4 *)(src + e);
+        return *(const RADAMW_GLOBAL f32x4 *)(src + e);
+    };
+    double acc[4] = {0.0, 0.0, 0.0, 0.0};
+    int64_t i = s;
+    for (; i + 3 * JOIN_STRIPS < count; i += 4 * JOIN_STRIPS) {
+        f32x4 v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) v[u] = at(i + u * JOIN_STRIPS);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[j] += static_cast<double>(v[u][j]);
+    }
+    for (; i < count; i += JOIN_STRIPS) {
+        const f32x4 v = at(i);
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[j] += static_cast<double>(v[j]);
     }
@@ -214,7 +359,7 @@ __device__ __forceinline__ void join_rows(const float *first, const float *rest,
     if (threadIdx.x < JOIN_COLUMNS) {
         double v = 0.0;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) v += strip[k][threadIdx.x];
+        for (int k = 0; k < JOIN_STRIPS; ++k) v += strip[k][threadIdx.x];
         const int64_t col = int64_t(blockIdx.x) * JOIN_COLUMNS + threadIdx.x;
         if (col < dim) {
             const float f = static_cast<float>(v);
@@ -251,15 +396,28 @@ __global__ __launch_bounds__(JOIN_BLOCK) void residual_join(ResidualGradArgs a, 
 
 template <int SDT, int BDT, int NT, int K>
 static void residual_grad_at(const ResidualGradArgs &a, const ResidualPlan &p, hipStream_t stream) {
-    const auto kernel = a.dim % 8 ? residual_norm_grad<SDT, BDT, NT, K, true> : residual_norm_grad<SDT, BDT, NT, K, false>;
+    auto kernel = a.dim % 8 ? residual_norm_grad<SDT, BDT, NT, K, true, 0> : residual_norm_grad<SDT, BDT, NT, K, false, 0>;
+    const uint32_t has = (a.pre ? HAS_PRE : 0) | (a.post ? HAS_POST : 0) | (a.gate ? HAS_GATE : 0) |
+                         (a.branch ? HAS_BRANCH : 0) | (a.grad_h ? HAS_GRAD_H : 0) |
+                         (a.gate && a.per == 1 ? EACH_ROW : 0) |
+                         (a.grad_gate ? a.per == 1 ? EACH_GATE : SUM_GATE : 0);
+    if constexpr (K == 1) {
+        if (a.dim == NT * 8) {
+            constexpr uint32_t PLAIN = HAS_PRE | HAS_BRANCH | HAS_GRAD_H, BOTH = PLAIN | HAS_POST,
+                               EACH = BOTH | HAS_GATE | EACH_ROW | EACH_GATE;
+            if (has == EACH) kernel = residual_norm_grad<SDT, BDT, NT, K, false, EACH>;
+            else if ((has & ~(HAS_GATE | SUM_GATE)) == BOTH) kernel = residual_norm_grad<SDT, BDT, NT, K, false, BOTH>;
+            else if ((has & ~(HAS_GATE | SUM_GATE)) == PLAIN) kernel = residual_norm_grad<SDT, BDT, NT, K, false, PLAIN>;
+        }
+    }
     hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(ceil_div(p.workers, row_block<NT> / NT))), dim3(row_block<NT>), 0,
-                       stream, a, p);
+                       stream, a, p, has);
 }
 
 template <int SDT, int BDT>
 static hipError_t residual_grad_rows(const ResidualGradArgs &a, const ResidualPlan &p, hipStream_t stream) {
 #define RADAMW_CALL(NT, K) residual_grad_at<SDT, BDT, NT, K>(a, p, stream)
-    RADAMW_ROW_SHAPES(a.dim, RADAMW_CALL)
+    RADAMW_ROW_SHAPES(a.dim, RADAMW_CALL, RADAMW_CALL(1024, 1))
 #undef RADAMW_CALL
     return hipGetLastError();
 }

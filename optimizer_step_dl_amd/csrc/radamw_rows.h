@@ -150,11 +150,13 @@ __device__ __forceinline__ void stream8(void *p, int64_t e, f32x8 v) {
 
 // Eight values at column e < dim of a row; columns from dim on read as zeros
 // and are not stored.  TAIL: dim may be no multiple of eight.  SHARED: other
-// workgroups read the data as well, so that it is loaded without the
-// nontemporal hint.
+// workgroups read the data as well.  Such data, unaligned rows and FP32, whose
+// lines two loads share, are loaded without the nontemporal hint: dropout of
+// 4097 x 1111 FP32 values takes 8.2 us, against 10.2 us with it; 16-bit values
+// of aligned rows take less with it (32768 x 8192 BF16: 178 against 188 us).
 template <int DT, bool TAIL, bool SHARED = false>
 __device__ __forceinline__ Raw8<DT> load_piece(const void *row, int32_t e, int32_t dim) {
-    if (!TAIL || e + 8 <= dim) return SHARED ? load_raw8<DT>(row, e) : stream_raw8<DT>(row, e);
+    if (!TAIL || e + 8 <= dim) return SHARED || TAIL || DT == G_F32 ? load_raw8<DT>(row, e) : stream_raw8<DT>(row, e);
     uint32_t b[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) b[j] = e + j < dim ? load_bits<DT>(row, e + j) : 0u;
@@ -176,6 +178,57 @@ __device__ __forceinline__ void store_piece(void *row, int32_t e, int32_t dim, f
 #pragma unroll
     for (int j = 0; j < 8; ++j)
         if (e + j < dim) store_value<DT>(row, e + j, v[j]);
+}
+
+// Four values at column e, as two words (16-bit types) or four; zeros from dim
+// on.
+template <int DT, bool TAIL, bool SHARED>
+__device__ __forceinline__ u32x4 load_four(const void *row, int32_t e, int32_t dim) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    typedef u32x2 u32x2_any2 __attribute__((aligned(2)));
+    if (e + 4 <= dim) {
+        if constexpr (DT == G_F32) {
+            return SHARED || TAIL ? load_chunk<DT>(row, e) : stream_chunk<DT>(row, e);
+        } else {
+            const auto *p = (const RADAMW_GLOBAL u32x2_any2 *)(static_cast<const uint16_t *>(row) + e);
+            u32x2 v;
+            if constexpr (SHARED || TAIL) v = *p;
+            else v = __builtin_nontemporal_load(p);
+            return u32x4{v[0], v[1], 0, 0};
+        }
+    }
+    u32x4 r = {0, 0, 0, 0};
+    if constexpr (TAIL) {
+        uint32_t b[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) b[j] = e + j < dim ? load_bits<DT>(row, e + j) : 0u;
+        if constexpr (DT == G_F32) r = u32x4{b[0], b[1], b[2], b[3]};
+        else r = u32x4{b[0] | b[1] << 16, b[2] | b[3] << 16, 0, 0};
+    }
+    return r;
+}
+template <int DT, bool TAIL>
+__device__ __forceinline__ void store_four(void *row, int32_t e, int32_t dim, f32x4 v) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    typedef u32x2 u32x2_any2 __attribute__((aligned(2)));
+    typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+    if (e + 4 <= dim) {
+        if constexpr (DT == G_F32) {
+            stream_out<DT>(row, e, __builtin_bit_cast(u32x4, v));
+        } else {
+            u32x2 w;
+            if constexpr (DT == G_F16) w = __builtin_bit_cast(u32x2, __builtin_convertvector(v, f16x4));
+            else w = __builtin_bit_cast(u32x2, __builtin_convertvector(v, bf16x4));
+            __builtin_nontemporal_store(w, (RADAMW_GLOBAL u32x2_any2 *)(static_cast<uint16_t *>(row) + e));
+        }
+        return;
+    }
+    if constexpr (TAIL) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (e + j < dim) store_value<DT>(row, e + j, v[j]);
+    }
 }
 
 // Element `e` of an array whose elements' type is known at run time.
