@@ -23,7 +23,7 @@ LIB_PATH = os.path.join(HERE, "libradamw.so")
 SOURCES = ["radamw_api.cpp", "radamw_update.hip", "radamw_stats.hip", "radamw_staged.hip", "radamw_probe.hip",
            "radamw_vocab_api.cpp", "radamw_embedding.hip", "radamw_loss.hip",
            "radamw_block_api.cpp", "radamw_dropout.hip", "radamw_residual.hip",
-           "radamw_residual_grad.hip", "radamw_balance.hip"]
+           "radamw_residual_grad.hip", "radamw_residual_grad_f32.hip", "radamw_balance.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

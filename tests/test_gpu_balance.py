@@ -73,6 +73,10 @@ CASES = [
     dict(n=40, experts=2048, k=8, z=0.01), dict(n=40, experts=4096, k=8), dict(n=33, experts=4091, k=8, dtype=BF16),
     dict(n=70_001, experts=32, k=2, masked=0.1, z=0.001), dict(n=5000, experts=96, k=4, std=40.0),
     dict(n=5000, experts=96, k=4, std=40.0, score="sigmoid")]
+# one workgroup's batch and the next larger ones
+CASES += [dict(n=n, experts=e, k=3, dtype=d, z=0.01, masked=0.3) for n, e, d in
+          ((2048, 8, F32), (2049, 8, F32), (32, 512, BF16), (33, 512, F32), (103, 160, F32), (5461, 3, F16), (16384, 1, BF16))
+          if e >= 3 or d == BF16]
 GROUPED = [dict(n=300, experts=24, k=2, bounds=[0, 100, 100, 101, 300], z=0.01),
            dict(n=5000, experts=64, k=6, bounds=[7, 8, 2000, 2000, 4900], masked=0.3, score="sigmoid", weighted=True),
            dict(n=4096, experts=128, k=8, bounds=list(range(0, 4097, 64)), dtype=BF16, ids=torch.int32, weighted=True),

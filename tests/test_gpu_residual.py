@@ -140,6 +140,17 @@ CASES += [
     dict(n=3, dim=40, p=1.0, gate="column")]
 
 
+# rows that fill their lanes, with the parts that the gradient knows at compile time, and rows in pairs
+CASES += [dict(n=n, dim=d, stream=s, branch=b, weight=F32, gate=g, gate_type=b, per=7 if g == "sequence" else None, post=post,
+               p=p)
+          for n, d in ((70, 512), (300, 1024), (33, 2048), (20, 4096), (9, 8192))
+          for s, b in ((BF16, BF16), (F32, F16))
+          for g, post, p in (("element", True, 0.3), (None, True, 0.0), ("sequence", True, 0.2), ("column", False, 0.1))]
+CASES += [dict(n=2049, dim=d, stream=s, branch=b, weight=w, gate=g, gate_type=F32, per=3, p=0.2)
+          for d, s, b, w, g in ((100, F16, F16, F16, "sequence"), (1003, F32, BF16, F32, "column"), (260, F32, F32, F32, None),
+                                (2048, BF16, BF16, BF16, "element"))]
+
+
 @pytest.mark.parametrize("kw", CASES, ids=lambda kw: "-".join(str(v).replace("torch.", "") for v in kw.values()))
 def test_forward(kw):
     announce(f"residual forward {kw}")
