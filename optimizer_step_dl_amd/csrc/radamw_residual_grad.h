@@ -1,7 +1,7 @@
 // radamw_residual_grad.h -- the kernel of the gradient of the residual stream's norms
-// around one block (radamw_residual.hip) for gfx950; its two
-// translation units are radamw_residual_grad.hip (16-bit streams, the join and
-// the launches) and radamw_residual_grad_f32.hip.
+// around one block (radamw_residual.hip) for gfx950; radamw_residual_grad.hip
+// has the join, the launches and FP32 alone, the other types are compiled beside
+// it (radamw_residual_grad_*.hip).
 //
 //   D        = dh + r_h (q - hat_h mean(q hat_h)),  q = dout (o + w_pre),
 //                                                   hat_h = h r_h
@@ -334,7 +334,11 @@ hipError_t residual_grad_rows(const ResidualGradArgs &a, const ResidualPlan &p, 
     return hipGetLastError();
 }
 
-// FP32 streams, by the branch's type.
-hipError_t residual_grad_f32(const ResidualGradArgs &a, const ResidualPlan &p, int bdt, hipStream_t stream);
+// FP32 streams under 16-bit branches.
+hipError_t residual_grad_f32_f16(const ResidualGradArgs &a, const ResidualPlan &p, hipStream_t stream);
+hipError_t residual_grad_f32_bf16(const ResidualGradArgs &a, const ResidualPlan &p, hipStream_t stream);
+// 16-bit streams.
+hipError_t residual_grad_f16(const ResidualGradArgs &a, const ResidualPlan &p, hipStream_t stream);
+hipError_t residual_grad_bf16(const ResidualGradArgs &a, const ResidualPlan &p, hipStream_t stream);
 
 }  // namespace radamw

@@ -1,6 +1,6 @@
 // radamw_residual_grad.hip -- the gradient of the residual stream's norms
 // around one block for gfx950 (the kernel is in radamw_residual_grad.h): the
-// workers, 16-bit streams, the join of the workers' sums, the launches.
+// workers, FP32 alone, the join of the workers' sums, the launches.
 #include "radamw_residual_grad.h"
 
 namespace radamw {
@@ -106,9 +106,9 @@ hipError_t launch_residual_grad(const ResidualGradArgs &a, const ResidualPlan &p
                                 int *launched) {
     hipError_t e = hipSuccess;
     if (a.n > 0) {
-        if (sdt == G_F32) e = residual_grad_f32(a, p, bdt, stream);
-        else if (bdt == G_F16) e = residual_grad_rows<G_F16, G_F16>(a, p, stream);
-        else e = residual_grad_rows<G_BF16, G_BF16>(a, p, stream);
+        if (sdt == G_F32 && bdt == G_F32) e = residual_grad_rows<G_F32, G_F32>(a, p, stream);
+        else if (sdt == G_F32) e = bdt == G_F16 ? residual_grad_f32_f16(a, p, stream) : residual_grad_f32_bf16(a, p, stream);
+        else e = bdt == G_F16 ? residual_grad_f16(a, p, stream) : residual_grad_bf16(a, p, stream);
         if (e != hipSuccess) return e;
         ++*launched;
     }
