@@ -191,6 +191,11 @@ __device__ __forceinline__ void rows_of_piece(const BalanceArgs &a, const Balanc
 #pragma unroll
     for (int k = 0; k < K; ++k) acc[k] = f32x8{};
     if constexpr (GRAD) {
+        // The probabilities add up to one, so that a number taken off every
+        // count leaves the gradient as it is.  Taken off as whole numbers, the
+        // count of a balanced router leaves the small differences that the
+        // gradient is made of with all their digits: a balanced one is zero.
+        const int32_t even = static_cast<int32_t>(a.tokens[piece.group] * a.top_k / a.experts);
         const double t = max(a.tokens[piece.group], 1);
         double up = a.grad_scale / t;
         if (a.weights) up *= a.weights[piece.group];
@@ -203,7 +208,7 @@ __device__ __forceinline__ void rows_of_piece(const BalanceArgs &a, const Balanc
             const Piece8 e = columns_of<SPLIT>(lane, k, lg);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                cost[k][j] = e.at(j) < experts ? f * static_cast<float>(a.counts[piece.group * a.experts + e.at(j)]) : 0.0f;
+                cost[k][j] = e.at(j) < experts ? f * static_cast<float>(a.counts[piece.group * a.experts + e.at(j)] - even) : 0.0f;
         }
     }
     for (int64_t t = piece.begin + mine; t < piece.end; t += per) {

@@ -176,6 +176,26 @@ def test_all_rows_masked():
     assert float(got["total"]) == 0 and not got["counts"].any() and not got["grad"].any()
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_a_balanced_router_has_no_gradient(score):
+    """Experts that are chosen equally often cost the same: the gradient is a
+    difference of equal terms, and exactly zero."""
+    announce(f"balance of a balanced router {score}")
+    x, _, _ = inputs(1557, 6, 1)
+    ids = torch.arange(6).expand(1557, 6).contiguous()
+    for grad in (True, False):
+        got = run(x, ids, None, bounds=[0, 500, 1557], score=score, grad=grad)
+        assert not got["grad"].any() and bool((got["counts"] == got["tokens"][:, None]).all())
+    # one choice more of one expert: the difference has all its digits, up to the probabilities' own error.  It is 1 /
+    # 1557 of the count, and the bound of the sum over all of it 1557 times as large as what is asked for here.
+    ids = ids.clone()
+    ids[0, 0] = 1
+    ref = balance(x, ids, score=score)["grad"][0]
+    got = run(x, ids, score=score)["grad"].cpu().double()
+    # probabilities: 80 u (3 u |x| and 70 u of the sum among them), twice in a product, and the products' roundings
+    assert float((got - ref).abs().max()) <= 400 * 2.0 ** -24 * float(ref.abs().max())
+
+
 def test_counts_summed_over_ranks():
     """Gradients from counts and tokens that two halves of a batch summed are
     the whole batch's."""
