@@ -40,7 +40,10 @@ def _rows(t: torch.Tensor) -> torch.Tensor:
     t = t.reshape(-1, t.shape[-1])
     row, col = t.stride()
     rows, cols = t.shape
-    return t if (cols == 1 or col == 1) and (rows <= 1 or row >= cols) else t.contiguous()
+    if (cols == 1 or col == 1) and (rows <= 1 or row >= cols):
+        return t
+    # contiguous() would keep the strides of a tensor without rows, whatever they are
+    return t.clone(memory_format=torch.contiguous_format)
 
 
 def _flat32(t: Optional[torch.Tensor], what: str, n: int) -> Optional[torch.Tensor]:
