@@ -309,7 +309,8 @@ class _ResidualNorm(torch.autograd.Function):
         rstd = _empty32((2, n), dev)
         h = None if branch is None else torch.empty((n, dim), dtype=x.dtype, device=dev)
         out = None if pre_weight is None else torch.empty((n, dim), dtype=out_dtype, device=dev)
-        given = [None if t is None else t.detach() for t in (x, branch, gate, post_weight, pre_weight)]
+        # without rows there is no gate row for the call to read
+        given = [None if t is None else t.detach() for t in (x, branch, gate if n else None, post_weight, pre_weight)]
         _abi.radamw_residual_norm(given[0], given[1], opts, gate=given[2], rows_per_gate=per, post_weight=given[3],
                                   pre_weight=given[4], h=h, out=out, rstd=rstd)
         # h is read again by the norm before the next block alone
@@ -339,13 +340,18 @@ class _ResidualNorm(torch.autograd.Function):
         grad_x = torch.empty((n, dim), dtype=stream, device=dev)
         grad_branch = empty(branch)
         grad_gate, grad_post, grad_pre = empty(gate, asked[2]), empty(post_weight, asked[3]), empty(pre_weight, asked[4])
+        gate_out = grad_gate
+        if n == 0:  # as in the forward call; the gate's gradient is a sum over no rows
+            gate_out = gate = None
+            if grad_gate is not None:
+                grad_gate.zero_()
         need = _abi.radamw_residual_grad_workspace_bytes(n, dim, ctx.per or 1)
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         _abi.radamw_residual_norm_grad(
             h, branch, ctx.opts, rstd, workspace, gate=gate, rows_per_gate=ctx.per, post_weight=post_weight,
             pre_weight=pre_weight, grad_h=None if grad_h is None else _rows(grad_h),
             grad_out=None if grad_out is None else _rows(grad_out), grad_x=grad_x, grad_branch=grad_branch,
-            grad_gate=grad_gate, grad_post_weight=grad_post, grad_pre_weight=grad_pre)
+            grad_gate=gate_out, grad_post_weight=grad_post, grad_pre_weight=grad_pre)
         return grad_x, grad_branch, grad_gate, grad_post, grad_pre, None, None, None
 
 
