@@ -910,7 +910,8 @@ int radamw_residual_norm_grad(const radamw_residual_block *block, const void *h,
  *             the device; other values are clamped to 0 .. n for every
  *             access, but the result is unspecified).  Rows outside every
  *             group take no part.  NULL: one group (groups = 1) of all rows.
- *   weights : groups FP32, or NULL: all 1.  A group of weight 0 adds nothing.
+ *   weights : groups FP32, or NULL: all 1.  A group of weight 0 adds nothing to
+ *             the total, and its gradient is zeros, whatever its logits hold.
  *   opts    : host; coefficients >= 0, finite; z_coef 0 with sigmoid scores.
  *   total   : 1 FP32.  loss : groups FP32.
  *   counts  : [groups, experts] int32.  tokens : groups int32 (T).

@@ -146,6 +146,7 @@ __device__ __forceinline__ void rows_of_piece(const BalanceArgs &a, const Balanc
     const int32_t experts = static_cast<int32_t>(a.experts);
     f32x8 cost[K], acc[K];
     float zc = 0.0f, sq = 0.0f;
+    bool counted = true;  // whether the group's loss is part of the total
 #pragma unroll
     for (int k = 0; k < K; ++k) acc[k] = f32x8{};
     if constexpr (GRAD) {
@@ -156,7 +157,10 @@ __device__ __forceinline__ void rows_of_piece(const BalanceArgs &a, const Balanc
         const int32_t even = static_cast<int32_t>(a.tokens[piece.group] * a.top_k / a.experts);
         const double t = max(a.tokens[piece.group], 1);
         double up = a.grad_scale / t;
-        if (a.weights) up *= a.weights[piece.group];
+        if (a.weights) {
+            up *= a.weights[piece.group];
+            counted = a.weights[piece.group] != 0.0f;
+        }
         if (a.upstream) up *= *a.upstream;
         zc = static_cast<float>(2.0 * a.z_coef * up);
         const float f = static_cast<float>(up * a.balance_coef * static_cast<double>(a.experts) /
@@ -237,7 +241,7 @@ __device__ __forceinline__ void rows_of_piece(const BalanceArgs &a, const Balanc
                 for (int j = 0; j < 8; ++j) {
                     g[j] = x[k][j] * (cost[k][j] - inner);
                     if constexpr (SIGMOID) g[j] *= rest[k][j];
-                    if (!live) g[j] = 0.0f;
+                    if (!live || !counted) g[j] = 0.0f;  // whatever the logits hold
                 }
                 store_piece<DT, SPLIT, TAIL>(elem_at(a.grad, DT, t * a.grad_stride), e, experts, g);
             }
