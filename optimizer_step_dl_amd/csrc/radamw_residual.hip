@@ -21,6 +21,21 @@
 
 namespace radamw {
 
+// Of a branch whose reciprocal root is NaN dropout may drop every column of the
+// row and yet keep some that lie behind it in the last lanes' pieces, which are
+// no part of the row's sum.  So such a root is taken into the row's own values,
+// all of them NaN then, and 1 is left of it.
+template <int DT>
+__device__ __forceinline__ void take_nan(Raw8<DT> &r, float &root, Piece e, int32_t dim) {
+    root = 1.0f;
+#pragma unroll
+    for (int j = 0; j < 8; j += DT == G_F32 ? 1 : 2) {
+        const int32_t c = j < 4 ? e.e + j : e.e2 + j - 4;
+        if constexpr (DT == G_F32) r.c[j / 4][j % 4] = c < dim ? 0x7fc00000u : 0u;
+        else r.c[0][j / 2] = (c < dim ? 0x7fffu : 0u) | (c + 1 < dim ? 0x7fff0000u : 0u);
+    }
+}
+
 // NT lanes hold a row, K pieces of eight each.
 template <int SDT, int BDT, int NT, int K, bool TAIL>
 __global__ __launch_bounds__(row_block<NT>) void residual_norm(ResidualArgs a, int64_t row0) {
@@ -72,6 +87,10 @@ __global__ __launch_bounds__(row_block<NT>) void residual_norm(ResidualArgs a, i
         s = row_sum<NT>(s, part[0]);
         rb = rsqrtf(__builtin_fmaf(s, inv_dim, a.eps));
         if (a.rstd && lane == 0) a.rstd[t] = rb;
+        if ((SPLIT || TAIL) && rb != rb) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) take_nan<BDT>(y[k], rb, piece_at<SPLIT, NT>(lane, k), dim);
+        }
     }
     f32x8 h[K];
     float s = 0.0f;
@@ -164,6 +183,11 @@ __global__ __launch_bounds__(row_block<NT>) void residual_norm_pair(ResidualArgs
             rb[m] = rsqrtf(__builtin_fmaf(s[m], inv_dim, a.eps));
             if (a.rstd && lane == 0) a.rstd[t[m]] = rb[m];
             s[m] = 0.0f;
+        }
+        if ((SPLIT || TAIL) && (rb[0] != rb[0] || rb[1] != rb[1])) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+                if (rb[m] != rb[m]) take_nan<BDT>(y[m], rb[m], e, dim);
         }
     }
     f32x8 h[2];
