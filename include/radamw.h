@@ -922,7 +922,7 @@ int radamw_residual_norm_grad(const radamw_residual_block *block, const void *h,
  * A group without rows has loss 0.  A row whose logits are all -inf (or whose
  * scores are all 0, as FP64 numbers: sigmoid logits below -709.78) adds no
  * probability and has a zero gradient.
- * n * top_k <= 2^31 - 16 and groups below 2^24 (RADAMW_ERR_RANGE).
+ * n * top_k <= 2^31 - 16 and groups <= 2^24 - 2048 (RADAMW_ERR_RANGE).
  *
  * radamw_balance_grad is the gradient from the forward call's counts and
  * tokens, for a backward pass that learns its scale (upstream, 1 FP32 on the

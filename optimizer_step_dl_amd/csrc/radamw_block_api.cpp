@@ -16,7 +16,8 @@ using namespace radamw;
 namespace {
 
 constexpr int64_t MAX_DROPOUT_DIM = int64_t(1) << 24;
-constexpr int64_t MAX_LAUNCH_BLOCKS = (int64_t(1) << 24) - 1;
+// With the at most 1024 pieces of a batch this is below 2^24 workgroups.
+constexpr int64_t MAX_GROUPS = (int64_t(1) << 24) - 2048;
 
 int check_drop(const radamw_dropout_options &o, int64_t n, DropArgs *d) {
     if (!(o.p >= 0.0 && o.p <= 1.0) || o.first_row < 0) return RADAMW_ERR_INVALID;
@@ -85,8 +86,7 @@ int check_balance(int64_t n, int64_t experts, int64_t stride, int dt, int idt, i
     if ((rc = finite_scale(grad_scale))) return rc;
     if (top_k < 1 || groups < 1 || (!offsets && groups != 1)) return RADAMW_ERR_INVALID;
     if ((rc = check_rows(n, experts, stride, BALANCE_MAX_EXPERTS))) return rc;
-    if (top_k > MAX_ROWS || n > MAX_ROWS / top_k || groups > MAX_LAUNCH_BLOCKS) return RADAMW_ERR_RANGE;
-    return balance_plan(n, experts, groups).pieces > MAX_LAUNCH_BLOCKS ? RADAMW_ERR_RANGE : RADAMW_OK;
+    return top_k > MAX_ROWS || n > MAX_ROWS / top_k || groups > MAX_GROUPS ? RADAMW_ERR_RANGE : RADAMW_OK;
 }
 
 }  // namespace
@@ -242,7 +242,7 @@ int64_t radamw_balance_workspace_bytes(int64_t n, int64_t experts, int64_t group
     int rc;
     if ((rc = check_rows(n, experts, experts, BALANCE_MAX_EXPERTS))) return rc;
     if (groups < 1) return RADAMW_ERR_INVALID;
-    if (groups > MAX_LAUNCH_BLOCKS) return RADAMW_ERR_RANGE;
+    if (groups > MAX_GROUPS) return RADAMW_ERR_RANGE;
     return balance_plan(n, experts, groups).bytes;
 }
 
