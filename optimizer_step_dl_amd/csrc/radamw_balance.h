@@ -91,6 +91,15 @@ __device__ __forceinline__ Piece8 columns_of(int lane, int k, int lg) {
     else return {{(lane + (k << lg)) * 8, (lane + (k << lg)) * 8 + 4}};
 }
 
+// exp(d) for d <= 0.  log2 e is in two parts: as one FP32 number it is too
+// small by 1.3e-8, and every exponential of d too large by that much of -d.
+// The first has 13 bits, so that the second is many steps of the exponent's
+// last digit and rounds evenly.
+constexpr float LOG2E_HI = 5909.0f / 4096, LOG2E_LO = static_cast<float>(1.4426950408889634 - 5909.0 / 4096);
+__device__ __forceinline__ float exp_of(float d) {
+    return __builtin_amdgcn_exp2f(__builtin_fmaf(d, LOG2E_LO, d * LOG2E_HI));
+}
+
 // The scores of a row that are all far below one, anew and in proportion: with
 // the largest logit m taken off every exponent, exp(x - m) / (1 + exp(x)), what
 // FP32 would hold as zeros (logits below -87) keeps its share of the sum, which
@@ -124,8 +133,7 @@ __device__ __forceinline__ float far_scores(const void *row, int lane, int lg, i
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float v = x[k][j];
-            x[k][j] = __builtin_amdgcn_exp2f((v - top) * LOG2E);
-            x[k][j] *= __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * LOG2E));  // exp(v) < 2^-6
+            x[k][j] = exp_of(v - top) * __builtin_amdgcn_rcpf(1.0f + exp_of(v));  // exp(v) < 2^-6
             sum += x[k][j];
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -196,7 +204,7 @@ __device__ __forceinline__ void rows_of_piece(const BalanceArgs &a, const Balanc
             for (int k = 0; k < K; ++k)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float v = x[k][j], e = __builtin_amdgcn_exp2f(-fabsf(v) * LOG2E), r = 1.0f / (1.0f + e);
+                    const float v = x[k][j], e = exp_of(-fabsf(v)), r = 1.0f / (1.0f + e);
                     x[k][j] = v >= 0.0f ? r : e * r;  // NaN stays NaN: e is
                     rest[k][j] = v >= 0.0f ? e * r : r;
                     sum += x[k][j];
@@ -211,7 +219,7 @@ __device__ __forceinline__ void rows_of_piece(const BalanceArgs &a, const Balanc
             for (int k = 0; k < K; ++k)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    x[k][j] = __builtin_amdgcn_exp2f((x[k][j] - m) * LOG2E);
+                    x[k][j] = exp_of(x[k][j] - m);
                     sum += x[k][j];
                 }
             sum = lanes_sum(sum, lg);
