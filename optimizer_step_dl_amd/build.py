@@ -20,8 +20,9 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(HERE, "libradamw.so")
-SOURCES = ["radamw_balance.hip", "radamw_balance_sigmoid.hip", "radamw_residual_grad_f32_bf16.hip", "radamw_residual_grad_f32_f16.hip",  # the longest first
-           "radamw_residual_grad.hip", "radamw_residual_grad_bf16.hip", "radamw_residual_grad_f16.hip", "radamw_residual.hip",
+SOURCES = ["radamw_balance.hip", "radamw_balance_sigmoid.hip",  # the longest first
+           "radamw_residual_grad_f32_bf16.hip", "radamw_residual_grad_f32_f16.hip", "radamw_residual_grad.hip",
+           "radamw_residual_grad_bf16.hip", "radamw_residual_grad_f16.hip", "radamw_residual.hip",
            "radamw_api.cpp", "radamw_update.hip", "radamw_stats.hip", "radamw_staged.hip", "radamw_probe.hip",
            "radamw_vocab_api.cpp", "radamw_embedding.hip", "radamw_loss.hip", "radamw_block_api.cpp", "radamw_dropout.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -14,10 +14,11 @@
 //
 // The gradient needs all counts, so ids are counted first (they are an eighth
 // of the logits' bytes or less); then loss and gradient take one read of the
-// logits and one write.  Bound by HBM where the batch is long: 262144 x 256
-// FP32 logits with their gradient take 132 us (554 MB: 4.2 TB/s), 112 us of it
-// in balance_rows, the rest in the count and the two joins; by the latency of
-// five dependent launches where it is not (16383 x 160 in 13 groups: 34 us).
+// logits and one write.  262144 x 256 FP32 logits with their gradient take 132
+// us (554 MB: 4.2 TB/s), 107 us of it in balance_rows (537 MB: 5.0 TB/s), the
+// rest in the count, the joins and the loss.  16383 x 160 in 13 groups take 33
+// us, 19 us of it in balance_rows: there a row's mask, logits, sums over lanes
+// and store wait for one another, and five launches do.
 #include "radamw_balance.h"
 
 namespace radamw {
@@ -35,7 +36,7 @@ BalancePlan balance_plan(int64_t n, int64_t experts, int64_t groups) {
     BalancePlan p{};
     // one piece of up to 16384 values, which one workgroup does in one launch;
     // of more, at least 512 pieces where that leaves each 2048 values, and
-    // about 1024 of a long batch: 16383 x 160 take 34 us, against 40 us with
+    // about 1024 of a long batch: 16383 x 160 take 33 us, against 40 us with
     // 256 pieces; 262144 x 256 take 132 us, against 157 us with 2048
     if (n <= ceil_div(16384, experts)) p.rows = max_of(1, n);
     else p.rows = max_of(ceil_div(n, 1024), max_of(ceil_div(2048, experts), min_of(ceil_div(n, 512), ceil_div(16384, experts))));

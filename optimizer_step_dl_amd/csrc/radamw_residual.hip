@@ -225,7 +225,8 @@ __global__ __launch_bounds__(row_block<NT>) void residual_norm_pair(ResidualArgs
     }
 }
 
-// Two rows at a time where that leaves four workgroups per CU: 8192 x 4096
+// Two rows at a time where that leaves four workgroups per CU (up to 512
+// columns one, of eight rows): 8192 x 4096
 // (FP32 stream, BF16 branch, FP32 weights) takes 77 us, against 84 us, 65536 x
 // 2048 BF16 186 against 197 us.  Wider rows have no registers for two.
 constexpr int64_t PAIR_ROWS = 2048;

@@ -460,7 +460,9 @@ def balance_loss(logits: torch.Tensor, ids: torch.Tensor, *, mask: Optional[torc
     them all rows are one group.  ``total`` is differentiable with respect to
     the logits alone; ``loss`` (groups), ``counts`` [groups, experts] (int32)
     and ``mean_prob`` [groups, experts] are not.  ``weights`` default to 1 /
-    groups."""
+    groups.  The counts are those of these rows: a loss over the rows of several
+    processes takes radamw_balance_loss, sums of its counts and tokens, and
+    radamw_balance_grad."""
     if ids.shape[:-1] != logits.shape[:-1]:
         raise ValueError(f"ids have shape {tuple(ids.shape)}, expected {tuple(logits.shape[:-1])} + (top_k,)")
     if mask is not None and mask.shape != logits.shape[:-1]:

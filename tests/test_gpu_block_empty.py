@@ -8,7 +8,7 @@ from optimizer_step_dl_amd.functional import balance_loss, dropout, embedding, p
 
 pytestmark = pytest.mark.gpu
 
-F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+F32, BF16 = torch.float32, torch.bfloat16
 
 
 @pytest.mark.parametrize("shape", [(0, 24), (3, 0, 24), (0, 5, 24)])
@@ -35,7 +35,7 @@ def test_inputs_without_rows():
     total = policy_loss(none, labels, values)[0] + balance_loss(none, labels[:, None].expand(0, 2))[0] + \
         residual_norm(none, none).sum() + dropout(none, 0.5, seed=1).sum()
     total.backward()
-    assert float(total) == 0 and bool((x.grad == 0).all())
+    assert float(total.detach()) == 0 and bool((x.grad == 0).all())
 
 
 @pytest.mark.parametrize("post,pre", [(True, True), (True, False), (False, True), (False, False)])
